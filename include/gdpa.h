@@ -319,6 +319,172 @@ GDPA_API gdpa_status_t gdpa_window_bwd(int32_t B, int32_t h, int32_t dh, int64_t
                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The attention layer around gdpa_window_fwd: rotary positions, a paged cache
+ * of keys and values for serving, attention of new tokens over that cache,
+ * and the norms around a block.  The Kunlun pages name the sequence's
+ * self-attention only (section 2.2, sliding-window bullet); these calls are
+ * what a layer of it needs in training and in serving.  They read offsets as
+ * the calls above do, except that rows t >= offsets[B] (a padded batch) are
+ * allowed: such rows of an output are left as they were.
+ */
+
+/*
+ * Rotary positions.  Within the first `rot` elements of a head, pair i (0 <= i <
+ * rot / 2) is (x[2i], x[2i+1]) when interleaved, else (x[i], x[i + rot/2]), and
+ * (a, b) becomes mscale * (a cos t - b sin t, a sin t + b cos t), t = pos * w_i:
+ *     w_i = base^(-2i/rot) * (g_i + (1 - g_i) / factor),
+ *     g_i = clamp((trained_len * base^(-2i/rot) / (2 pi) - low) / (high - low), 0, 1)
+ * (g_i = 0 when trained_len = 0: every frequency is divided by `factor`).
+ * Elements from rot on are copied.
+ */
+typedef struct {
+  int32_t rot;           /* rotated elements of a head: even, 2 .. dh */
+  int32_t interleaved;   /* 1: pairs (2i, 2i+1), 0: pairs (i, i + rot/2) */
+  int32_t trained_len;   /* context length of training, for the piecewise scaling; 0: none */
+  int32_t reserved;      /* 0 */
+  double base;           /* >= 1, e.g. 10000 */
+  double factor;         /* >= 1; 1: no scaling */
+  double low, high;      /* turns within trained_len below / above which a frequency is
+                            divided by factor / kept (low < high) */
+  double mscale;         /* scale of the rotated elements, e.g. 1 */
+} gdpa_rotary_t;
+
+/*
+ * Rotates x [T, h, dh] into y (bf16 or fp32, `dtype`; fp32 arithmetic, one rounding).
+ *   Position of token t: positions[t] (int32 [T], any sign) when given; else, for t
+ *   of sample b by offsets [B+1], kv_len[b] - n_b + (t - offsets[b]) (kv_len
+ *   int32 [B]: the sample's length with its n_b new tokens), or t - offsets[b]
+ *   without kv_len.  Exactly one of kv_len / positions may be given; with
+ *   positions alone offsets may be NULL (B is ignored), and every row turns.
+ *   x_stride, y_stride: elements between tokens (>= h * dh, multiples of 16
+ *   bytes), so that heads of a fused projection rotate in place; y may be x
+ *   (with the same stride).  dh = 32, 64 or 128.
+ *   inverse = 1: the transposed map, which is the gradient (dy in, dx out).
+ * Angles are reduced exactly (64-bit fixed-point turns) at every position.
+ */
+GDPA_API gdpa_status_t gdpa_rotary(const gdpa_rotary_t* r, int32_t dtype, int32_t B, int32_t h,
+                                   int32_t dh, int64_t total_tokens, const int32_t* offsets,
+                                   const int32_t* kv_len, const int32_t* positions,
+                                   const void* x, int64_t x_stride, void* y, int64_t y_stride,
+                                   int32_t inverse, void* stream);
+
+/*
+ * A paged cache of bf16 keys and values: k, v [num_pages, hk, page, dh] (device,
+ * 16-byte aligned), page_table int32 [B, max_pages] (device): the position p of
+ * sample b lies in page page_table[b][p / page], row p % page.  Entries of
+ * pages that a call does not touch may hold anything.  page: a power of two, 16 .. 1024;
+ * dh = 32, 64 or 128; max_pages * page < 2^31.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* page_table;
+  int32_t num_pages, max_pages, page, hk, dh;
+  int32_t reserved;      /* 0 */
+} gdpa_cache_t;
+
+/*
+ * Appends the new tokens' keys and values to the cache, rotating the keys (and
+ * the queries) on the way; r may be NULL (no rotation).
+ *   kv_len int32 [B]: tokens of each sample WITH the n_b = offsets[b+1] -
+ *   offsets[b] new ones; new token i of sample b has position kv_len[b] - n_b +
+ *   i.  A token with a negative position (left padding) is not stored.
+ *   k, v [T, hk, dh] with k_stride / v_stride elements between tokens; q
+ *   [T, hq, dh] (q_stride) -> q_out [T, hq, dh] contiguous; q and q_out both or
+ *   neither.  Strides are multiples of 8.  No two tokens may share a cache row.
+ *   status_ws: NULL, or a device buffer of >= 256 bytes, 256-byte aligned,
+ *   whose status word is cleared and receives GDPA_ERR_INVALID_ARG when a token
+ *   lies past the page table or in a page outside [0, num_pages) (it is then
+ *   not stored); read with gdpa_workspace_status.
+ */
+GDPA_API gdpa_status_t gdpa_cache_append(const gdpa_rotary_t* r, const gdpa_cache_t* cache,
+                                         int32_t B, int32_t hq, int64_t total_tokens,
+                                         const int32_t* offsets, const int32_t* kv_len,
+                                         const void* q, int64_t q_stride, void* q_out,
+                                         const void* k, int64_t k_stride, const void* v,
+                                         int64_t v_stride, void* status_ws, void* stream);
+
+/*
+ * Attention of each sample's new tokens over its cached keys and values: the
+ * serving form of gdpa_window_fwd.  New token i of sample b (position p_i =
+ * kv_len[b] - n_b + i; the cache holds its own key too) attends to the positions
+ * max(0, p_i - window + 1) .. p_i:
+ *     O_i = sum_p softmax_p(scale * q_i . k_p) v_p,   LSE_i = ln sum_p exp(scale * q_i . k_p)
+ * Query head j reads kv head j / (hq / hk).  A token that sees nothing (a negative
+ * position) gets O = 0 and LSE = -inf.
+ *   q, o bf16 [T, hq, dh]; lse fp32 [hq, T] (may be NULL); offsets, kv_len as in
+ *   gdpa_cache_append.  window >= 1 (2^31 - 1: plain causal attention).  hq a
+ *   multiple of hk, hq / hk <= 128.  max_n: upper bound of the n_b (selects the kernel).
+ *   Cache rows that no new token of the sample sees may hold anything (NaN too), and pages
+ *   without such rows need no valid table entry.
+ *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned;
+ *   its status word receives GDPA_ERR_INVALID_ARG for offsets that decrease,
+ *   leave [0, T] or exceed max_n (the sample is skipped), and for a kv_len past
+ *   the page table or a page outside [0, num_pages) among those it reads (the
+ *   sample's outputs are then undefined; nothing outside the cache is read).
+ * Reproducible: the same inputs give the same bits.
+ */
+GDPA_API gdpa_status_t gdpa_chunk_workspace_size(const gdpa_cache_t* cache, int32_t B, int32_t hq,
+                                                 int64_t total_tokens, int32_t max_n,
+                                                 size_t* bytes);
+GDPA_API gdpa_status_t gdpa_chunk_fwd(const gdpa_cache_t* cache, int32_t B, int32_t hq,
+                                      int64_t total_tokens, int32_t max_n, int32_t window,
+                                      float scale, const void* q, const int32_t* offsets,
+                                      const int32_t* kv_len, void* o, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gate of gdpa_block_norm_fwd: none, one per element, or one row per sample. */
+typedef enum { GDPA_GATE_NONE = 0, GDPA_GATE_TOKEN = 1, GDPA_GATE_SAMPLE = 2 } gdpa_gate_t;
+
+typedef struct {
+  int64_t T;             /* rows (tokens), 0 <= T < 2^31 */
+  int32_t d;             /* width, 1 .. 8192 */
+  int32_t dtype;         /* gdpa_dtype_t of x, f, gate, y, n and their gradients */
+  int32_t gate;          /* gdpa_gate_t */
+  int32_t sigmoid;       /* 1: act(z) = 1 / (1 + exp(-z)), 0: act(z) = z */
+  int32_t B;             /* samples (sample gates only) */
+  float alpha;           /* residual scale */
+  float eps;             /* >= 0, inside the root */
+  int32_t reserved;      /* 0 */
+} gdpa_block_norm_t;
+
+/*
+ * Norms before and after a block, with its gate and residual scale: with x [T, d]
+ * the residual stream and f [T, d] the block's output,
+ *     u = w_post * f / rms(f)  (u = f without w_post),   rms(v) = sqrt(mean(v^2) + eps),
+ *     y = x + alpha * act(gate) * u  (act = 1 without a gate),   n = w_pre * y / rms(y).
+ *   gate: [T, d], or [B, d] shared by a sample's rows (offsets [B+1]; rows behind
+ *   the last sample are left as they were).  w_post, w_pre fp32 [d].  y may be x.
+ *   f NULL (then no gate, w_post, y): n = w_pre * x / rms(x).  w_pre NULL: no n.
+ *   Base pointers 16-byte aligned (offsets 4-byte).
+ * Statistics and sums are fp32, and n is taken from y before y is rounded.
+ */
+GDPA_API gdpa_status_t gdpa_block_norm_fwd(const gdpa_block_norm_t* p, const int32_t* offsets,
+                                           const void* x, const void* f, const void* gate,
+                                           const float* w_post, const float* w_pre, void* y,
+                                           void* n, void* stream);
+
+/*
+ * Gradient of gdpa_block_norm_fwd for dy of y and dn of n (y: the forward's y,
+ * or x where f is NULL; read with w_pre only):
+ *   dx, df [T, d]; dgate [T, d] like the gate, or fp32 [B, d] for a sample gate
+ *   (zero for a sample without rows); dw_post, dw_pre fp32 [d].
+ *   dy may be NULL (zero) when dn is given; dn goes with w_pre.
+ *   workspace: device, >= gdpa_block_norm_bwd_workspace_size bytes, 256-byte aligned.
+ * Reproducible: the same inputs give the same bits (no atomics).
+ */
+GDPA_API gdpa_status_t gdpa_block_norm_bwd_workspace_size(const gdpa_block_norm_t* p,
+                                                          size_t* bytes);
+GDPA_API gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const int32_t* offsets,
+                                           const void* y, const void* f, const void* gate,
+                                           const float* w_post, const float* w_pre,
+                                           const void* dy, const void* dn, void* dx, void* df,
+                                           void* dgate, float* dw_post, float* dw_pre,
+                                           void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
+/*
  * Device-detected status of the last gdpa_fwd/gdpa_bwd that used `workspace`
  * (GDPA_OK, GDPA_ERR_INVALID_ARG for inconsistent offsets, GDPA_ERR_TIMEOUT).
  * Synchronises `stream`; writes the code to *status (host).

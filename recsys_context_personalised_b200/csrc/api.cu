@@ -33,6 +33,8 @@ KernelScope::~KernelScope() {
   if (rec >= 0) cudaEventRecord(g_recs[rec].stop, st);
 }
 
+void reset_launch_count() { g_launches = 0; }
+
 static void clear_records() {
   for (auto& r : g_recs) {
     if (r.start) cudaEventDestroy(r.start);
@@ -140,6 +142,18 @@ gdpa_status_t cuda_status(cudaError_t e) {
 }
 
 }  // namespace
+
+gdpa_status_t check_cache(const gdpa_cache_t* c, int32_t B) {
+  if (!c || !c->k || !c->v || !c->page_table) return GDPA_ERR_INVALID_ARG;
+  if (B < 1 || c->hk < 1 || c->num_pages < 1 || c->max_pages < 1) return GDPA_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || ((uintptr_t)c->page_table & 3u))
+    return GDPA_ERR_INVALID_ARG;
+  if (c->dh != 32 && c->dh != 64 && c->dh != 128) return GDPA_ERR_UNSUPPORTED;
+  if (c->page < 16 || c->page > 1024 || (c->page & (c->page - 1))) return GDPA_ERR_UNSUPPORTED;
+  if ((int64_t)c->max_pages * c->page >= (int64_t)1 << 31 || c->hk > 4096)
+    return GDPA_ERR_UNSUPPORTED;
+  return GDPA_OK;
+}
 }  // namespace gdpa
 
 using namespace gdpa;

@@ -105,6 +105,18 @@ cudaError_t launch_bias_prep(const gdpa_problem_t& p, const int32_t* offsets, co
                              const void* g, const float* b2, float* dsum, float* db1,
                              float* db2, const WsHeader* ws, cudaStream_t st);
 
+// Starts the launch count of an entry point (gdpa_last_launch_count).
+void reset_launch_count();
+// SMs of the current device.
+int device_sm_count();
+// Checks a paged cache's description for a call on B samples.
+gdpa_status_t check_cache(const gdpa_cache_t* c, int32_t B);
+inline int log2_int(int x) {
+  int n = 0;
+  while ((1 << (n + 1)) <= x) ++n;
+  return n;
+}
+
 // Brackets one kernel launch: counts it for gdpa_last_launch_count() and, while
 // gdpa_timing_enable(1) is in force, records CUDA events around it on `st`.
 struct KernelScope {

@@ -43,6 +43,29 @@ class KernelTime(ctypes.Structure):
                 ("total_ms", ctypes.c_float)]
 
 
+class RotarySpec(ctypes.Structure):
+    """Mirror of gdpa_rotary_t."""
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("trained_len", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+class Cache(ctypes.Structure):
+    """Mirror of gdpa_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("hk", ctypes.c_int32), ("dh", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class BlockNorm(ctypes.Structure):
+    """Mirror of gdpa_block_norm_t."""
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("sigmoid", ctypes.c_int32), ("B", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 class GdpaError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where}: {STATUS.get(code, code)}")
@@ -104,6 +127,19 @@ def load(path: str = LIB_PATH):
     lib.gdpa_window_bwd_workspace_size.restype = ctypes.c_int
     lib.gdpa_window_bwd.argtypes = [i32, i32, i32, i64, i32, i32, f32] + [vp] * 11 + [sz, vp]
     lib.gdpa_window_bwd.restype = ctypes.c_int
+    rp, cp, np_ = (ctypes.POINTER(x) for x in (RotarySpec, Cache, BlockNorm))
+    psz = ctypes.POINTER(sz)
+    lib.gdpa_rotary.argtypes = [rp, i32, i32, i32, i32, i64, vp, vp, vp, vp, i64, vp, i64, i32, vp]
+    lib.gdpa_cache_append.argtypes = [rp, cp, i32, i32, i64, vp, vp, vp, i64, vp, vp, i64, vp, i64,
+                                      vp, vp]
+    lib.gdpa_chunk_workspace_size.argtypes = [cp, i32, i32, i64, i32, psz]
+    lib.gdpa_chunk_fwd.argtypes = [cp, i32, i32, i64, i32, i32, f32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.gdpa_block_norm_fwd.argtypes = [np_] + [vp] * 9
+    lib.gdpa_block_norm_bwd_workspace_size.argtypes = [np_, psz]
+    lib.gdpa_block_norm_bwd.argtypes = [np_] + [vp] * 14 + [sz, vp]
+    for name in ("rotary", "cache_append", "chunk_workspace_size", "chunk_fwd", "block_norm_fwd",
+                 "block_norm_bwd_workspace_size", "block_norm_bwd"):
+        getattr(lib, "gdpa_" + name).restype = ctypes.c_int
     for name in EXPORTED[:8]:
         getattr(lib, name).restype = ctypes.c_int
     if path == LIB_PATH:
@@ -379,6 +415,291 @@ def window_bwd(q: torch.Tensor, offsets, k: torch.Tensor, v: torch.Tensor, o: to
     if rc:
         raise GdpaError(rc, "gdpa_window_bwd")
     return dq, dk, dv
+
+
+def _need(ok, where: str, what: str) -> None:
+    if not ok:
+        raise GdpaError(1, f"{where} ({what})")
+
+
+def _operand(where, name, t, dtype, shape, device) -> None:
+    """A contiguous tensor of that type and shape on `device`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
+            and tuple(t.shape) == shape and t.is_contiguous()):
+        raise GdpaError(1, f"{where} ({name}: a contiguous {dtype} tensor {list(shape)} on {device})")
+
+
+def _heads(where, name, t, dtype, shape, device) -> int:
+    """A [T, h, dh] tensor whose heads are contiguous; returns its token stride."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
+            and t.dim() == 3 and tuple(t.shape) == shape and t.stride(2) == 1
+            and (t.stride(1) == shape[2] or shape[1] == 1)):
+        raise GdpaError(1, f"{where} ({name}: {dtype} {list(shape)} on {device}, heads contiguous)")
+    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+
+class _On:
+    """Makes a tensor's device current, and `stream` (when given) the stream
+    that allocations belong to, for the length of a call."""
+
+    def __init__(self, where, t, stream):
+        _need(isinstance(t, torch.Tensor) and t.is_cuda, where, "a CUDA tensor")
+        self.raw = None
+        self.ctx = []
+        if t.device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(t.device))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+                stream = torch.cuda.ExternalStream(raw, device=t.device)
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def rotary_spec(rot: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
+                trained_len: int = 0, low: float = 1.0, high: float = 32.0,
+                mscale: float = 1.0) -> RotarySpec:
+    """Rotary settings: ``rot`` rotated elements of a head, pairs (2i, 2i+1) when
+    ``interleaved`` else (i, i + rot/2), frequencies base^(-2i/rot) divided by
+    ``factor``; with ``trained_len`` only the frequencies that make fewer than
+    ``high`` turns within it (fully below ``low`` turns) are."""
+    return RotarySpec(int(rot), int(bool(interleaved)), int(trained_len), 0, float(base),
+                      float(factor), float(low), float(high), float(mscale))
+
+
+def rotary(spec: RotarySpec, x: torch.Tensor, offsets=None, kv_len=None, positions=None, out=None,
+           inverse: bool = False, stream=None) -> torch.Tensor:
+    """Run gdpa_rotary: x [T, h, dh] (bf16 or fp32, heads contiguous, any token
+    stride) rotated by ``positions`` [T], or by each token's place in its sample
+    (``offsets`` [B+1]; with ``kv_len`` [B] the sample ends at that length).
+    ``out`` may be ``x``; rows behind the last sample are left as they were (in a
+    new ``out``: not set).  ``inverse`` gives the gradient."""
+    w = "gdpa_rotary"
+    with _On(w, x, stream) as st:
+        _need(x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32), w,
+              "x: bf16 or fp32 [T, h, dh]")
+        T, h, dh = x.shape
+        xs = _heads(w, "x", x, x.dtype, (T, h, dh), x.device)
+        B = 0
+        if offsets is not None:
+            B = offsets.numel() - 1
+            _operand(w, "offsets", offsets, torch.int32, (B + 1,), x.device)
+        if kv_len is not None:
+            _operand(w, "kv_len", kv_len, torch.int32, (B,), x.device)
+        if positions is not None:
+            _operand(w, "positions", positions, torch.int32, (T,), x.device)
+        if out is None:
+            out = torch.empty((T, h, dh), dtype=x.dtype, device=x.device)
+        ys = _heads(w, "out", out, x.dtype, (T, h, dh), x.device)
+        rc = load().gdpa_rotary(ctypes.byref(spec), DTYPE_BF16 if x.dtype == torch.bfloat16
+                                else DTYPE_F32, B, h, dh, T, _ptr(offsets), _ptr(kv_len),
+                                _ptr(positions), _ptr(x), xs, _ptr(out), ys, int(bool(inverse)), st)
+    if rc:
+        raise GdpaError(rc, w)
+    return out
+
+
+def _cache(where, cache_k, cache_v, page_table, B) -> Cache:
+    _need(isinstance(cache_k, torch.Tensor) and cache_k.dim() == 4, where,
+          "cache_k: [num_pages, hk, page, dh]")
+    pages, hk, page, dh = cache_k.shape
+    dev = cache_k.device
+    _operand(where, "cache_k", cache_k, torch.bfloat16, (pages, hk, page, dh), dev)
+    _operand(where, "cache_v", cache_v, torch.bfloat16, (pages, hk, page, dh), dev)
+    _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, where,
+          "page_table: [B, max_pages]")
+    _operand(where, "page_table", page_table, torch.int32, (B, page_table.shape[1]), dev)
+    return Cache(_ptr(cache_k), _ptr(cache_v), _ptr(page_table), pages, page_table.shape[1], page,
+                 hk, dh, 0)
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v,
+                 spec: Optional[RotarySpec] = None, q=None, q_out=None, status_ws=None,
+                 stream=None) -> Optional[torch.Tensor]:
+    """Run gdpa_cache_append: rotates (``spec``) and stores the new tokens' keys
+    and values k, v [T, hk, dh] in the paged cache [num_pages, hk, page, dh];
+    ``kv_len`` [B] counts each sample's tokens with the new ones.  With ``q``
+    [T, hq, dh] its rotation is returned (``q_out``)."""
+    w = "gdpa_cache_append"
+    with _On(w, cache_k, stream) as st:
+        dev = cache_k.device
+        _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
+        B = offsets.numel() - 1
+        c = _cache(w, cache_k, cache_v, page_table, B)
+        _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
+        _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
+        T = k.shape[0]
+        ks = _heads(w, "k", k, torch.bfloat16, (T, c.hk, c.dh), dev)
+        vs = _heads(w, "v", v, torch.bfloat16, (T, c.hk, c.dh), dev)
+        hq, qs = 0, 0
+        if q is not None:
+            hq = q.shape[1]
+            qs = _heads(w, "q", q, torch.bfloat16, (T, hq, c.dh), dev)
+            if q_out is None:
+                q_out = torch.empty((T, hq, c.dh), dtype=q.dtype, device=dev)
+            _operand(w, "q_out", q_out, torch.bfloat16, (T, hq, c.dh), dev)
+        else:
+            _need(q_out is None, w, "q_out without q")
+        if status_ws is not None:
+            _need(status_ws.is_cuda and status_ws.device == dev and status_ws.is_contiguous()
+                  and status_ws.numel() * status_ws.element_size() >= 256, w,
+                  "status_ws: 256 bytes on the device")
+        rc = load().gdpa_cache_append(None if spec is None else ctypes.byref(spec), ctypes.byref(c),
+                                      B, hq, T, _ptr(offsets), _ptr(kv_len), _ptr(q), qs,
+                                      _ptr(q_out), _ptr(k), ks, _ptr(v), vs, _ptr(status_ws), st)
+    if rc:
+        raise GdpaError(rc, w)
+    return q_out
+
+
+def chunk_workspace_bytes(cache: Cache, B: int, hq: int, T: int, max_n: int) -> int:
+    n = ctypes.c_size_t()
+    rc = load().gdpa_chunk_workspace_size(ctypes.byref(cache), B, hq, T, max_n, ctypes.byref(n))
+    if rc:
+        raise GdpaError(rc, "gdpa_chunk_workspace_size")
+    return n.value
+
+
+def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, scale: float,
+              max_n: int, window: Optional[int] = None, o=None, lse=None, ws=None,
+              want_lse: bool = True, stream=None):
+    """Run gdpa_chunk_fwd: attention of the new tokens q [T, hq, dh] over each
+    sample's ``kv_len`` cached tokens (its own among them), causal and, with
+    ``window``, limited to the last ``window`` tokens; ``max_n`` bounds the new
+    tokens of a sample.  Returns (o [T, hq, dh], lse fp32 [hq, T] or None)."""
+    w = "gdpa_chunk_fwd"
+    with _On(w, q, stream) as st:
+        dev = q.device
+        _need(q.dim() == 3, w, "q: [T, hq, dh]")
+        T, hq, dh = q.shape
+        _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
+        B = offsets.numel() - 1
+        c = _cache(w, cache_k, cache_v, page_table, B)
+        _operand(w, "q", q, torch.bfloat16, (T, hq, c.dh), cache_k.device)
+        _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
+        _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _operand(w, "o", o, torch.bfloat16, (T, hq, dh), dev)
+        if lse is not None:
+            _operand(w, "lse", lse, torch.float32, (hq, T), dev)
+        elif want_lse:
+            lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = workspace(chunk_workspace_bytes(c, B, hq, T, max_n), dev)
+        else:
+            _need(ws.is_cuda and ws.device == dev and ws.dtype == torch.uint8
+                  and ws.is_contiguous(), w, "ws: a contiguous uint8 tensor on the device")
+        rc = load().gdpa_chunk_fwd(ctypes.byref(c), B, hq, T, max_n,
+                                   0x7fffffff if window is None else window, scale, _ptr(q),
+                                   _ptr(offsets), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(ws),
+                                   ws.numel(), st)
+    if rc:
+        raise GdpaError(rc, w)
+    return o, lse
+
+
+def _block_norm(where, x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid) -> BlockNorm:
+    """Checks the operands of a block norm and fills its description."""
+    _need(isinstance(x, torch.Tensor) and x.dim() == 2
+          and x.dtype in (torch.bfloat16, torch.float32), where, "x: bf16 or fp32 [T, d]")
+    T, d = x.shape
+    _operand(where, "x", x, x.dtype, (T, d), x.device)
+    if f is not None:
+        _operand(where, "f", f, x.dtype, (T, d), x.device)
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        if t is not None:
+            _operand(where, name, t, torch.float32, (d,), x.device)
+    kind, B = 0, 0
+    if gate is not None:
+        kind = 1 if offsets is None else 2
+        B = 0 if offsets is None else offsets.numel() - 1
+        _operand(where, "gate", gate, x.dtype, (T if kind == 1 else B, d), x.device)
+    if offsets is not None:
+        _need(gate is not None, where, "offsets go with a gate shared by a sample's rows")
+        _operand(where, "offsets", offsets, torch.int32, (B + 1,), x.device)
+    return BlockNorm(T, d, DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, kind,
+                     int(bool(sigmoid)), B, alpha, eps, 0)
+
+
+def block_norm_fwd(x: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, offsets=None,
+                   alpha: float = 1.0, eps: float = 1e-6, sigmoid: bool = False, y=None, n=None,
+                   stream=None):
+    """Run gdpa_block_norm_fwd: y = x + alpha * act(gate) * (w_post * f / rms(f)),
+    n = w_pre * y / rms(y), on [T, d] rows (bf16 or fp32; weights fp32 [d]).
+    ``gate`` [T, d], or with ``offsets`` [B+1] one row [B, d] per sample;
+    without ``w_post`` f enters as it is, without ``w_pre`` there is no n, without
+    ``f`` y is x.  Returns (y, n)."""
+    w = "gdpa_block_norm_fwd"
+    with _On(w, x, stream) as st:
+        p = _block_norm(w, x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid)
+        if f is None:
+            _need(y is None, w, "y without f")
+        elif y is None:
+            y = torch.empty_like(x)
+        else:
+            _operand(w, "y", y, x.dtype, tuple(x.shape), x.device)
+        if w_pre is None:
+            _need(n is None, w, "n without w_pre")
+        elif n is None:
+            n = torch.empty_like(x)
+        else:
+            _operand(w, "n", n, x.dtype, tuple(x.shape), x.device)
+        rc = load().gdpa_block_norm_fwd(ctypes.byref(p), _ptr(offsets), _ptr(x), _ptr(f),
+                                        _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(n), st)
+    if rc:
+        raise GdpaError(rc, w)
+    return (x if f is None else y), n
+
+
+def block_norm_bwd(y: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, dy=None, dn=None,
+                   offsets=None, alpha: float = 1.0, eps: float = 1e-6, sigmoid: bool = False,
+                   dx=None, df=None, dgate=None, ws=None, stream=None):
+    """Run gdpa_block_norm_bwd for dy of y and dn of n (``y``: the forward's y, or
+    x where there is no f); returns (dx, df, dgate, dw_post, dw_pre), None where
+    there is no such operand.  dgate of a sample gate is fp32 [B, d]."""
+    w = "gdpa_block_norm_bwd"
+    lib = load()
+    with _On(w, y, stream) as st:
+        p = _block_norm(w, y, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid)
+        shape, dev = tuple(y.shape), y.device
+        _need((dn is None) == (w_pre is None), w, "dn goes with w_pre")
+        for name, t in (("dy", dy), ("dn", dn)):
+            if t is not None:
+                _operand(w, name, t, y.dtype, shape, dev)
+        dx = torch.empty_like(y) if dx is None else dx
+        _operand(w, "dx", dx, y.dtype, shape, dev)
+        if f is not None:
+            df = torch.empty_like(y) if df is None else df
+            _operand(w, "df", df, y.dtype, shape, dev)
+        if gate is not None:
+            gt = torch.float32 if offsets is not None else y.dtype
+            if dgate is None:
+                dgate = torch.empty(gate.shape, dtype=gt, device=dev)
+            _operand(w, "dgate", dgate, gt, tuple(gate.shape), dev)
+        dw_post, dw_pre = (None if t is None else torch.empty_like(t) for t in (w_post, w_pre))
+        n = ctypes.c_size_t()
+        rc = lib.gdpa_block_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n))
+        if rc:
+            raise GdpaError(rc, "gdpa_block_norm_bwd_workspace_size")
+        if ws is None:
+            ws = workspace(n.value, dev)
+        rc = lib.gdpa_block_norm_bwd(ctypes.byref(p), _ptr(offsets), _ptr(y), _ptr(f), _ptr(gate),
+                                     _ptr(w_post), _ptr(w_pre), _ptr(dy), _ptr(dn), _ptr(dx),
+                                     _ptr(df), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
+                                     ws.numel(), st)
+    if rc:
+        raise GdpaError(rc, w)
+    return dx, df, dgate, dw_post, dw_pre
 
 
 def workspace_status(ws: torch.Tensor, stream=None) -> int:
