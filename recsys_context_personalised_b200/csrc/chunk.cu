@@ -516,14 +516,12 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 a.lse[(int64_t)(head0 + h) * a.T + t] =
                     l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
             } else {
-              // rows of a piece lie one after another: token-major, nh heads
-              const int64_t at_row = at * a.rows + tk * nh + h;
-              float* dst = a.po + at_row * DH + t4 * 2;
+              float* dst = a.po + at * a.rows * DH + ((t4 >> 1) * a.rows + r) * 4 + (t4 & 1) * 2;
 #pragma unroll
               for (int n = 0; n < DH / 8; ++n)
-                *reinterpret_cast<float2*>(dst + n * 8) =
+                *reinterpret_cast<float2*>(dst + n * 8 * a.rows) =
                     make_float2(o[mt][n][2 * row], o[mt][n][2 * row + 1]);
-              if (t4 == 0) a.ml[at_row] = make_float2(top, l);
+              if (t4 == 0) a.ml[at * a.rows + r] = make_float2(top, l);
             }
           }
       }
@@ -542,13 +540,18 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 }
 
 // Joins the pieces of the item that begins in worker blockIdx.x's part and ends
-// in a later one: a warp per row, pieces in the workers' order.
+// in a later one: 8 rows at a time, a warp to 16 columns of every SPLIT-th piece, pieces merged
+// in the workers' order, then the splits in theirs.
+constexpr int kJoinThreads = 512;
 template <int DH>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinThreads)
 chunk_join_kernel(const ChunkArgs a, WsHeader* ws) {
+  constexpr int GROUPS = DH / 16, SPLIT = kJoinThreads / 32 / GROUPS;
+  __shared__ float4 sacc[SPLIT][GROUPS][32];
+  __shared__ float2 sml[SPLIT][GROUPS][8];
+  __shared__ int worst;
   const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (w == 0 && blockIdx.y == 0) {
-    __shared__ int worst;
     if (threadIdx.x == 0) worst = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < a.workers; i += blockDim.x)
@@ -557,70 +560,82 @@ chunk_join_kernel(const ChunkArgs a, WsHeader* ws) {
     if (threadIdx.x == 0) ws->status = worst;
   }
   const ChunkPiece first = a.piece[2 * w + 1];
-  if (first.tokens == 0 || w + 1 >= a.workers) return;
-  const int rows = first.tokens * first.heads;
-  const int r = blockIdx.y * 4 + warp;
-  if (r >= rows) return;
-  int last = w + 1;                                         // worker of the item's last piece
-  while (last + 1 < a.workers && !a.piece[2 * last].ends && a.piece[2 * last].tokens) ++last;
-  // the rows' max over the pieces, 32 pieces at a time
-  auto index = [&](int i) { return ((int64_t)(i == w ? 2 * w + 1 : 2 * i)) * a.rows + r; };
-  float top = -INFINITY;
-  for (int i = w + lane; i <= last; i += 32) top = fmaxf(top, a.ml[index(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float off = top == -INFINITY ? 0.f : top;
-  constexpr int PER = DH / 32;
-  float acc[PER], l = 0.f;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-#pragma unroll 4
-  for (int i = w; i <= last; ++i) {
-    const int64_t at = index(i);
-    const float2 ml = a.ml[at];
-    const float f = sm100::ex2_approx(ml.x - off);
-    l = fmaf(ml.y, f, l);
-#pragma unroll
-    for (int k = 0; k < PER; ++k) acc[k] = fmaf(a.po[at * DH + k * 32 + lane], f, acc[k]);
+  if (first.tokens == 0) return;
+  // worker of the item's last piece: the next one that holds the item's end
+  int last = w + 1;
+  for (; last < a.workers; last += 32) {
+    const int i = last + lane;
+    const bool stop = i >= a.workers - 1 || a.piece[2 * i].ends || a.piece[2 * i].tokens == 0;
+    const uint32_t m = __ballot_sync(0xffffffffu, stop);
+    if (m) {
+      last += __ffs(m) - 1;
+      break;
+    }
   }
-  const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-  const int tk = r / first.heads, h = r - tk * first.heads;
-  const int64_t t = first.token0 + tk;
+  last = min(last, a.workers - 1);
+  const int cg = warp % GROUPS, sp = warp / GROUPS, r8 = lane & 7, c4 = lane >> 3;
+  for (int r0 = blockIdx.y * 8; r0 < a.rows; r0 += gridDim.y * 8) {
+    const int r = r0 + r8, x = r / a.tile_rows, rr = r - x * a.tile_rows;
+    const int tk = rr / a.vgroup, h = rr - tk * a.vgroup;
+    const bool live = tk < a.rt1 && x * a.rt1 + tk < first.tokens && h < first.heads;
+    if (__syncthreads_or(live) == 0) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+#pragma unroll 4
+      for (int i = w + sp; i <= last; i += SPLIT) {
+        const int64_t at = i == w ? 2 * w + 1 : 2 * i;
+        const float2 ml = a.ml[at * a.rows + r];
+        const float4 v = *reinterpret_cast<const float4*>(
+            a.po + at * a.rows * DH + ((int64_t)(cg * 4 + c4) * a.rows + r) * 4);
+        if (ml.y == 0.f) continue;                            // a piece that this row sees nothing of
+        const float top = fmaxf(m, ml.x);
+        const float f = sm100::ex2_approx(m - top), g = sm100::ex2_approx(ml.x - top);
+        m = top;
+        l = l * f + ml.y * g;
+        acc.x = acc.x * f + v.x * g;
+        acc.y = acc.y * f + v.y * g;
+        acc.z = acc.z * f + v.z * g;
+        acc.w = acc.w * f + v.w * g;
+      }
+      sacc[sp][cg][lane] = acc;
+      if (c4 == 0) sml[sp][cg][r8] = make_float2(m, l);
+    }
+    __syncthreads();
+    if (live && sp == 0) {
 #pragma unroll
-  for (int k = 0; k < PER; ++k)
-    a.o[(t * a.hq + first.head0 + h) * DH + k * 32 + lane] = __float2bfloat16_rn(acc[k] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(int64_t)(first.head0 + h) * a.T + t] =
-        l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+      for (int i = 1; i < SPLIT; ++i) {
+        const float2 ml = sml[i][cg][r8];
+        const float4 v = sacc[i][cg][lane];
+        if (ml.y == 0.f) continue;
+        const float top = fmaxf(m, ml.x);
+        const float f = sm100::ex2_approx(m - top), g = sm100::ex2_approx(ml.x - top);
+        m = top;
+        l = l * f + ml.y * g;
+        acc.x = acc.x * f + v.x * g;
+        acc.y = acc.y * f + v.y * g;
+        acc.z = acc.z * f + v.z * g;
+        acc.w = acc.w * f + v.w * g;
+      }
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const int64_t t = first.token0 + x * a.rt1 + tk;
+      *reinterpret_cast<uint2*>(a.o + (t * a.hq + first.head0 + h) * DH + (cg * 4 + c4) * 4) =
+          make_uint2(sm100::pack_bf16x2(acc.x * inv, acc.y * inv),
+                     sm100::pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (a.lse && cg == 0 && c4 == 0)
+        a.lse[(int64_t)(first.head0 + h) * a.T + t] =
+            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    __syncthreads();
+  }
 }
 
 template <int DH, int MT>
 cudaError_t launch_rows(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t st) {
   using C = Cfg<DH, MT>;
-  auto enc = tensor_map_encoder();
-  if (!enc) return cudaErrorInvalidValue;
-  const CUtensorMapSwizzle sw = DH < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUtensorMap mq, mk, mv;
-  {
-    const cuuint64_t dims[3] = {(cuuint64_t)DH, (cuuint64_t)a.hq, (cuuint64_t)a.T};
-    const cuuint64_t strides[2] = {(cuuint64_t)DH * 2, (cuuint64_t)a.hq * DH * 2};
-    const cuuint32_t box[3] = {(cuuint32_t)C::CH, (cuuint32_t)a.vgroup, (cuuint32_t)a.rt};
-    if (enc(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16*>(a.q), dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  const cuuint64_t dims[4] = {(cuuint64_t)DH, (cuuint64_t)c.page, (cuuint64_t)c.hk,
-                              (cuuint64_t)c.num_pages};
-  const cuuint64_t strides[3] = {(cuuint64_t)DH * 2, (cuuint64_t)c.page * DH * 2,
-                                 (cuuint64_t)c.hk * c.page * DH * 2};
-  const cuuint32_t box[4] = {(cuuint32_t)C::CH, (cuuint32_t)(c.page < kBN ? c.page : kBN), 1, 1};
-  for (int i = 0; i < 2; ++i)
-    if (enc(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, i ? c.v : c.k, dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+  const CUtensorMapSwizzle sw = DH < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  if (!chunk_maps(a, c, DH, C::CH, kBN, sw, &mq, &mk, &mv)) return cudaErrorInvalidValue;
   auto kern = chunk_rows_kernel<DH, MT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
   if (e != cudaSuccess) return e;
@@ -629,22 +644,27 @@ cudaError_t launch_rows(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t 
   return cudaGetLastError();
 }
 
-// How a call is cut.
+// How a call is cut.  `tiles`: the tcgen05 kernel of chunk_sm100.cu.
 struct ChunkLayout {
-  int mt, rows, vheads, vgroup, rt, workers;
+  bool tiles;
+  int mt, rows, tile_rows, vheads, vgroup, rt1, rt, workers;
   size_t status_off, piece_off, ml_off, po_off, total;
 };
 ChunkLayout chunk_layout(const gdpa_cache_t& c, int hq, int max_n) {
   ChunkLayout L;
   const int group = hq / c.hk;
-  // one row tile of 16 where it holds all of a sample's rows, else 32; a group of more
-  // heads than rows is split
-  L.mt = (int64_t)group * max_n <= 16 ? 1 : 2;
-  L.rows = 16 * L.mt;
-  L.vheads = (group + L.rows - 1) / L.rows;
+  // one row tile of 16, or of 32, where it holds all of a sample's rows; pairs of 128-row
+  // tiles on the tensor core's tcgen05 path beyond that
+  const int64_t need = (int64_t)group * max_n;
+  L.tiles = need > 32;
+  L.mt = need <= 16 ? 1 : 2;
+  L.tile_rows = L.tiles ? 128 : 16 * L.mt;
+  L.rows = L.tiles ? 256 : L.tile_rows;
+  L.vheads = (group + L.tile_rows - 1) / L.tile_rows;
   L.vgroup = (group + L.vheads - 1) / L.vheads;
-  L.rt = L.rows / L.vgroup;
-  L.workers = 2 * device_sm_count();
+  L.rt1 = L.tile_rows / L.vgroup;
+  L.rt = L.tiles ? 2 * L.rt1 : L.rt1;
+  L.workers = (L.tiles ? 1 : 2) * device_sm_count();
   L.status_off = sizeof(WsHeader);
   L.piece_off = align_up(L.status_off + 4 * (size_t)L.workers, 256);
   L.ml_off = align_up(L.piece_off + 2 * sizeof(ChunkPiece) * (size_t)L.workers, 256);
@@ -671,12 +691,35 @@ gdpa_status_t finish(cudaError_t e) {
 
 }  // namespace
 
+bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int bn,
+                CUtensorMapSwizzle sw, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  auto make = [&](CUtensorMap* m, int dims, const void* p, const cuuint64_t* size,
+                  const cuuint64_t* stride, const cuuint32_t* box) {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(p), size, stride, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const cuuint64_t row = (cuuint64_t)dh * 2;
+  const cuuint64_t qsize[3] = {(cuuint64_t)dh, (cuuint64_t)a.hq, (cuuint64_t)a.T};
+  const cuuint64_t qstride[2] = {row, a.hq * row};
+  const cuuint32_t qbox[3] = {(cuuint32_t)ch, (cuuint32_t)a.vgroup, (cuuint32_t)a.rt1};
+  const cuuint64_t size[4] = {(cuuint64_t)dh, (cuuint64_t)c.page, (cuuint64_t)c.hk,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t stride[3] = {row, c.page * row, (cuuint64_t)c.hk * c.page * row};
+  const cuuint32_t box[4] = {(cuuint32_t)ch, (cuuint32_t)(c.page < bn ? c.page : bn), 1, 1};
+  return make(q, 3, a.q, qsize, qstride, qbox) && make(k, 4, c.k, size, stride, box) &&
+         make(v, 4, c.v, size, stride, box);
+}
+
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st) {
   KernelScope ks_("gdpa_chunk_join", st);
-  const dim3 grid(a.workers, (a.rows + 3) / 4);
-  if (dh == 32) chunk_join_kernel<32><<<grid, 128, 0, st>>>(a, ws);
-  if (dh == 64) chunk_join_kernel<64><<<grid, 128, 0, st>>>(a, ws);
-  if (dh == 128) chunk_join_kernel<128><<<grid, 128, 0, st>>>(a, ws);
+  const dim3 grid(a.workers, a.rows < 64 ? a.rows / 8 : 8);
+  if (dh == 32) chunk_join_kernel<32><<<grid, kJoinThreads, 0, st>>>(a, ws);
+  if (dh == 64) chunk_join_kernel<64><<<grid, kJoinThreads, 0, st>>>(a, ws);
+  if (dh == 128) chunk_join_kernel<128><<<grid, kJoinThreads, 0, st>>>(a, ws);
   return cudaGetLastError();
 }
 
@@ -733,8 +776,10 @@ extern "C" gdpa_status_t gdpa_chunk_fwd(const gdpa_cache_t* cache, int32_t B, in
   a.max_n = max_n;
   a.window = window;
   a.rt = L.rt;
+  a.rt1 = L.rt1;
   a.rows = L.rows;
-  a.bn_shift = kBNShift;
+  a.tile_rows = L.tile_rows;
+  a.bn_shift = L.tiles ? 7 : kBNShift;
   a.num_pages = cache->num_pages;
   a.max_pages = cache->max_pages;
   a.page_shift = log2_int(cache->page);
@@ -743,7 +788,8 @@ extern "C" gdpa_status_t gdpa_chunk_fwd(const gdpa_cache_t* cache, int32_t B, in
   cudaError_t e;
 #define GDPA_ROWS(DH) \
   (L.mt == 1 ? launch_rows<DH, 1>(a, *cache, st) : launch_rows<DH, 2>(a, *cache, st))
-  e = cache->dh == 32 ? GDPA_ROWS(32) : cache->dh == 64 ? GDPA_ROWS(64) : GDPA_ROWS(128);
+  e = L.tiles ? launch_chunk_tiles(a, *cache, st)
+              : cache->dh == 32 ? GDPA_ROWS(32) : cache->dh == 64 ? GDPA_ROWS(64) : GDPA_ROWS(128);
 #undef GDPA_ROWS
   if (e == cudaSuccess) e = launch_chunk_join(a, cache->dh, (WsHeader*)workspace, st);
   return finish(e);

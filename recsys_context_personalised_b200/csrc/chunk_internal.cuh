@@ -18,7 +18,8 @@ constexpr uint64_t kChunkTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy
 // tokens = 0).  Its rows' (max in log2 units, sum) and unnormalised O are at the
 // same index of the workspace's ml and po arrays.
 struct __align__(16) ChunkPiece {
-  int32_t token0, tokens, head0, heads;   // rows: token-major, `heads` query heads from head0 on
+  // row r of a tile: token r / vgroup of the tile, head head0 + r % vgroup (< head0 + heads)
+  int32_t token0, tokens, head0, heads;
   int32_t ends;                           // this piece holds the item's last block
   int32_t pad[3];
 };
@@ -33,10 +34,11 @@ struct ChunkArgs {
   int32_t* status;           // [workers]
   ChunkPiece* piece;         // [2 * workers]: a part's first (0) and last (1) unfinished item
   float2* ml;                // [2 * workers, rows]
-  float* po;                 // [2 * workers, rows, dh]
+  float* po;                 // [2 * workers, dh / 4, rows, 4]
   int64_t T;
   int32_t B, hq, hk, vheads, group, vgroup;   // group = hq / hk, in vheads parts of vgroup heads
-  int32_t max_n, window, rt, rows, bn_shift;
+  int32_t max_n, window, bn_shift;
+  int32_t rt, rt1, rows, tile_rows;           // an item: rt tokens in tiles of rt1 tokens, rows in tiles of tile_rows
   int32_t num_pages, max_pages, page_shift;
   int32_t workers;
   float scale_log2;          // scale * log2(e)
@@ -132,6 +134,14 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, int worker, Chunk
   }
   __syncthreads();
 }
+
+// The tensor maps of a call: Q as boxes of rt1 tokens x vgroup heads, K and V
+// as boxes of the rows of a page that lie in one block of `bn` positions; `ch` elements wide.
+bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int bn,
+                CUtensorMapSwizzle sw, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v);
+
+// Many rows per sample (chunk_sm100.cu), one worker per SM.
+cudaError_t launch_chunk_tiles(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t st);
 
 // Joins the pieces of the items that a part's border cuts, and the workers'
 // status words into the workspace's (grid: workers x row groups).
