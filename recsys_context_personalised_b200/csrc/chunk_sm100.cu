@@ -15,14 +15,26 @@
 //
 // CTA = 12 warps, one per SM:
 //   warp 0      TMA producer: Q of a visit (a run of one item's blocks), K and V page by page
-//   warp 1      MMA issuer (one lane): per block PV_A(j), S_A(j+1), PV_B(j), S_B(j+1)
+//   warp 1      MMA issuer (one lane); dh <= 64: of tile A, and warp 3 of tile B
 //   warp 2      TMEM allocator; zeroes the V rows of an item's first and last block
 //               that no row of the item sees (0 * NaN would reach O through the product)
 //   warps 4-7   softmax of tile A, warps 8-11 of tile B (thread = row = TMEM lane)
 //
-// TMEM columns: S_A [0,128), S_B [128,256) (P_X, packed bf16, aliases the first 64
-// columns of S_X: S_X(j+1) is issued behind PV_X(j)), O_A [256, 256+dh), O_B [256+dh, 256+2dh).
+// TMEM columns: S_A [0,128), S_B [128,256), O_A [256, 256+dh), O_B [256+dh, 256+2dh).  dh <= 64:
+// P_X (packed bf16) at [384 + 64X, 448 + 64X), and S_X(j+1) is issued as soon as S_X(j) lies in
+// registers (EARLY).  dh = 128: P_X aliases the first 64 columns of S_X, so S_X(j+1) is issued
+// behind PV_X(j).  P goes out in two halves of 64 keys; the product of the
+// first half runs while the second is computed.
+//
+// Softmax: online, 64 keys at a time, the running offset kept while a half's maximum stays
+// within 2^8 of it (softmax does not depend on the offset, and 2^8 is far from overflow).
 // P is rounded to bf16, the precision of the MMA's operand; its sum l is taken before that.
+//
+// The code is kept short on purpose (rolled loops over halves and column groups): a launch
+// fetches it cold, and with both halves, the masked and the unmasked path and the tiles unrolled
+// the warps waited for instructions most of the time on short windows (0.28 ms for 48
+// sessions of up to 700 events in a 256-event window).
+#include <limits.h>
 #include <math.h>
 
 #include "chunk_internal.cuh"
@@ -55,16 +67,17 @@ struct CfgT {
   static constexpr uint32_t SW = DH < 64 ? kSw64 : kSw128;
   static constexpr uint32_t ATOM = 8 * ROWB;
   static constexpr int QST = DH == 128 ? 1 : 2;         // Q stages (a stage = tiles A and B)
-  static constexpr int NS = DH == 32 ? 16 : DH == 64 ? 8 : 4;   // K/V ring slots
+  static constexpr int NS = DH == 32 ? 16 : DH == 64 ? 10 : 5;   // K/V ring slots
   static constexpr int NV = 8;                          // barriers of V blocks that pass warp 2
-  static_assert(NS / 2 <= NV, "as many as V blocks in flight");
-  static constexpr uint32_t COL_S = 0, COL_O = 256;
-  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 8,
-                       B_OEMPTY = 10, B_DRAIN = 12, B_VRAW = 13, B_KVFULL = 13 + NV,
-                       B_KVEMPTY = 13 + NV + NS, NBAR = 13 + NV + 2 * NS;
-  static constexpr uint32_t OSTG_WARP = 32 * 128;       // epilogue staging of a softmax warp
-  static constexpr uint32_t OFF_Q = 0, OFF_KV = QST * 2 * TILEB, OFF_OSTG = OFF_KV + NS * TILEB,
-                            OFF_CTL = OFF_OSTG + 8 * OSTG_WARP;
+  static_assert((NS + 1) / 2 <= NV, "as many as V blocks in flight");
+  static constexpr bool EARLY = DH <= 64;               // P has columns of its own
+  static constexpr int NI = EARLY ? 2 : 1;              // MMA issuers
+  static constexpr uint32_t COL_S = 0, COL_O = 256, COL_P = EARLY ? 384 : 0, P_STEP = EARLY ? 64 : 128;
+  // SFREE: S read; PHALF: the product with P's first half done, PFREE: with all of P
+  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_SFREE = 6, B_PFULL = 8, B_PHALF = 12,
+                       B_PFREE = 14, B_OFULL = 16, B_OEMPTY = 18, B_DRAIN = 20, B_VRAW = 21,
+                       B_KVFULL = B_VRAW + NV, B_KVEMPTY = B_KVFULL + NS, NBAR = B_KVEMPTY + NS;
+  static constexpr uint32_t OFF_Q = 0, OFF_KV = QST * 2 * TILEB, OFF_CTL = OFF_KV + NS * TILEB;
   static constexpr uint32_t CTL_TMEM = 8 * NBAR, CTL_ABORT = CTL_TMEM + 4,
                             CTL_VISIT = (CTL_ABORT + 4 + 15) / 16 * 16,
                             CTL_BYTES = CTL_VISIT + QST * sizeof(Visit);
@@ -73,6 +86,15 @@ struct CfgT {
   static constexpr uint32_t SMEM = USED > 120u * 1024u ? USED : 120u * 1024u;
   static_assert(SMEM + 512 <= 232448u, "shared memory of a CTA, the static part with it");
 };
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -107,17 +129,21 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_QFULL + i), 1);
-      mbar_init(bar(C::B_QEMPTY + i), 10);     // the MMA issuer, warp 2 and the 8 softmax warps
+      mbar_init(bar(C::B_QEMPTY + i), 9 + C::NI);   // the MMA issuers, warp 2 and the 8 softmax warps
       mbar_init(bar(C::B_SFULL + i), 1);
-      mbar_init(bar(C::B_PFULL + i), 128);
+      mbar_init(bar(C::B_SFREE + i), 4);
+      mbar_init(bar(C::B_PFULL + i), 4);
+      mbar_init(bar(C::B_PFULL + 2 + i), 4);
+      mbar_init(bar(C::B_PHALF + i), 1);
+      mbar_init(bar(C::B_PFREE + i), 1);
       mbar_init(bar(C::B_OFULL + i), 1);
-      mbar_init(bar(C::B_OEMPTY + i), 128);
+      mbar_init(bar(C::B_OEMPTY + i), 4);
     }
-    mbar_init(bar(C::B_DRAIN), 1);
+    mbar_init(bar(C::B_DRAIN), C::NI);
     for (int i = 0; i < C::NV; ++i) mbar_init(bar(C::B_VRAW + i), 1);
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(bar(C::B_KVFULL + i), 1);
-      mbar_init(bar(C::B_KVEMPTY + i), 1);
+      mbar_init(bar(C::B_KVEMPTY + i), C::NI);
     }
     *abort_flag = 0;
     bad_page = 0;
@@ -277,93 +303,125 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
       }
-    } else if (warp == 1) {
-      // -------------------------------------------------------- MMA issuer
-      if (lane == 0 && count > 0) {
-        uint32_t slot = 0, phase = 0, vn = 0;
-        uint32_t pcnt[2] = {0u, 0u}, ocnt[2] = {0u, 0u};
-        Visit cur, nxt;
-        auto take = [&]() -> int {
-          if (!mbar_wait(bar(C::B_KVFULL + slot), phase, abort_flag, kChunkTimeoutNs)) return -1;
-          tc_fence_after();
-          const int r = (int)slot;
-          if (++slot == (uint32_t)C::NS) {
-            slot = 0;
-            phase ^= 1u;
-          }
-          return r;
-        };
-        auto sees = [](const Visit& v, int x, int j) { return j >= v.b0[x] && j < v.b1[x]; };
-        auto issue_s = [&](int x, int ks, uint32_t qs) {
-          const uint64_t a0 = smem_desc(sQ + (qs * 2 + x) * C::TILEB, 16, C::ATOM, C::SW);
-          const uint64_t b0 = smem_desc(sKV + ks * C::TILEB, 16, C::ATOM, C::SW);
-#pragma unroll
-          for (int k = 0; k < DH / 16; ++k) {
-            const uint32_t off = (k / (C::CH / 16)) * C::CHUNKB + (k % (C::CH / 16)) * 32;
-            mma_ss(tmem + C::COL_S + 128 * x, desc_advance(a0, off), desc_advance(b0, off), IDESC_S,
-                   k > 0 ? 1u : 0u);
-          }
-          mma_commit(bar(C::B_SFULL + x));
-        };
-        auto issue_pv = [&](int x, int vs, bool first, bool last) -> bool {
-          if (!mbar_wait(bar(C::B_PFULL + x), pcnt[x] & 1u, abort_flag, kChunkTimeoutNs)) return false;
-          ++pcnt[x];
-          if (first && !mbar_wait(bar(C::B_OEMPTY + x), (ocnt[x] & 1u) ^ 1u, abort_flag, kChunkTimeoutNs))
-            return false;
-          tc_fence_after();
-          const uint64_t v0 = smem_desc(sKV + vs * C::TILEB, C::CHUNKB, C::ATOM, C::SW);
-#pragma unroll
-          for (int k = 0; k < kBNT / 16; ++k)
-            mma_ts(tmem + C::COL_O + DH * x, tmem + C::COL_S + 128 * x + k * 8,
-                   desc_advance(v0, k * 2 * C::ATOM), IDESC_O, k > 0 || !first ? 1u : 0u);
-          if (last) {
-            mma_commit(bar(C::B_OFULL + x));
-            ++ocnt[x];
-          }
-          return true;
-        };
-        bool ok = open_visit(vn, cur);
-        uint32_t qs = 0;
-        int j = cur.u0;
-        if (ok) {
-          tc_fence_after();
-          const int k = take();
-          ok = k >= 0;
-          if (ok) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (sees(cur, x, j)) issue_s(x, k, qs);
-            mma_commit(bar(C::B_KVEMPTY + k));
-            if (j == cur.u1 - 1) mma_commit(bar(C::B_QEMPTY + qs));
-          }
+    } else if (warp == 1 || (C::EARLY && warp == 3)) {
+      // ------------------------------------------------------- MMA issuers
+      // Both tiles in one in-order stream, PV_A(j), S_A(j+1), PV_B(j), S_B(j+1); or (EARLY) a
+      // stream of its own for each tile, S_X(j+1), PV_X(j).  The whole warp walks the blocks and
+      // one elected lane issues: values that are the same in the warp (as a broadcast tells the compiler)
+      // stay in uniform registers, where the descriptors have to be; issued by a lane on its
+      // own branch a product took 85 to 100 cycles to issue.
+      auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+      const uint32_t tm = (uint32_t)uni((int)tmem);
+      const bool leader = elect_one();
+      const int x_lo = C::EARLY && uni(warp) == 3 ? 1 : 0, x_hi = C::EARLY ? x_lo : 1;
+      // a negative scale: the products of -Q, and its absolute value in the softmax
+      const uint32_t idesc_s = IDESC_S | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
+      uint32_t slot = 0, phase = 0, vn = 0, qs = 0, scnt = 0, pbit = 0, obit = 0;
+      auto wait = [&](int b, uint32_t parity) -> bool {
+        const bool w = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kChunkTimeoutNs));
+        tc_fence_after();
+        return w;
+      };
+      auto take = [&]() -> int {
+        if (!wait(C::B_KVFULL + slot, phase)) return -1;
+        const int r = (int)slot;
+        if (++slot == (uint32_t)C::NS) {
+          slot = 0;
+          phase ^= 1u;
         }
-        for (int64_t left = count; ok && left > 0; --left) {
-          const int v = take();
-          if (v < 0) break;
-          if (sees(cur, 0, j) && !issue_pv(0, v, j == cur.b0[0], j == cur.b1[0] - 1)) break;
-          int k = -1, nj = j + 1;
-          if (left > 1) {
-            nxt = cur;
-            if (nj == cur.u1) {
-              ++vn;
-              if (!open_visit(vn, nxt)) break;
-              tc_fence_after();
-              nj = nxt.u0;
-              qs = vn % C::QST;
+        return r;
+      };
+      const int64_t steps = ((int64_t)uni((int)(count >> 32)) << 32) | (uint32_t)uni((int)count);
+      // block j of the products with P, block nj (of a visit that may be the next one) of S
+      int j = -1, nj = -1, u1 = 0, cb0[2] = {0, 0}, cb1[2] = {0, 0}, nb0[2] = {0, 0}, nb1[2] = {0, 0};
+      bool ok = true;
+      for (int64_t it = 0; ok && it <= steps && steps > 0; ++it) {
+        int v = -1, k = -1;
+        if (it > 0) ok = (v = take()) >= 0;
+        if (ok && it < steps) {
+          if (++nj >= u1) {                                   // the next visit
+            qs = vn % C::QST;
+            ok = wait(C::B_QFULL + qs, (vn / C::QST) & 1u);
+            ++vn;
+            const Visit& r = visits[qs];
+            nj = uni(r.u0);
+            u1 = uni(r.u1);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              nb0[x] = uni(r.b0[x]);
+              nb1[x] = uni(r.b1[x]);
             }
-            k = take();
-            if (k < 0) break;
-            if (sees(nxt, 0, nj)) issue_s(0, k, qs);
           }
-          if (sees(cur, 1, j) && !issue_pv(1, v, j == cur.b0[1], j == cur.b1[1] - 1)) break;
-          mma_commit(bar(C::B_KVEMPTY + v));
-          if (left > 1) {
-            if (sees(nxt, 1, nj)) issue_s(1, k, qs);
-            mma_commit(bar(C::B_KVEMPTY + k));
-            if (nj == nxt.u1 - 1) mma_commit(bar(C::B_QEMPTY + qs));
-            cur = nxt;
-            j = nj;
+          ok = ok && (k = take()) >= 0;
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int x = x_lo; x <= x_hi; ++x) {
+          const int c0 = x ? cb0[1] : cb0[0], c1 = x ? cb1[1] : cb1[0];
+          const int n0 = x ? nb0[1] : nb0[0], n1 = x ? nb1[1] : nb1[0];
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if ((half == 0) == C::EARLY) {                    // S_X(nj)
+              if (k < 0 || nj < n0 || nj >= n1) continue;
+              if (C::EARLY) {
+                if (scnt > 0) ok = wait(C::B_SFREE + x, (scnt - 1) & 1u);
+                if (!ok) break;
+                ++scnt;
+              }
+              const uint64_t a0 = smem_desc(sQ + (qs * 2 + x) * C::TILEB, 16, C::ATOM, C::SW);
+              const uint64_t b0 = smem_desc(sKV + k * C::TILEB, 16, C::ATOM, C::SW);
+              if (leader) {
+#pragma unroll
+                for (int q = 0; q < DH / 16; ++q) {
+                  const uint32_t off = (q / (C::CH / 16)) * C::CHUNKB + (q % (C::CH / 16)) * 32;
+                  mma_ss(tm + C::COL_S + 128 * x, desc_advance(a0, off), desc_advance(b0, off), idesc_s,
+                         q > 0 ? 1u : 0u);
+                }
+                mma_commit(bar(C::B_SFULL + x));
+              }
+            } else {                                          // O_X += P_X(j) V(j)
+              if (v < 0 || j < c0 || j >= c1) continue;
+              const uint32_t bit = 1u << x;
+              const bool first = j == c0, last = j == c1 - 1;
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                ok = wait(C::B_PFULL + 2 * x + h, (pbit >> x) & 1u);
+                if (ok && h == 0 && first) ok = wait(C::B_OEMPTY + x, ((obit >> x) & 1u) ^ 1u);
+                if (!ok) break;
+                const uint64_t v0 = desc_advance(smem_desc(sKV + v * C::TILEB, C::CHUNKB, C::ATOM, C::SW),
+                                                 h * 8 * C::ATOM);
+                if (leader) {
+#pragma unroll
+                  for (int q = 0; q < 4; ++q)
+                    mma_ts(tm + C::COL_O + DH * x, tm + C::COL_P + C::P_STEP * x + h * 32 + q * 8,
+                           desc_advance(v0, q * 2 * C::ATOM), IDESC_O, q > 0 || h > 0 || !first ? 1u : 0u);
+                  if (h == 0) {
+                    mma_commit(bar(C::B_PHALF + x));
+                  } else {
+                    if (C::EARLY) mma_commit(bar(C::B_PFREE + x));
+                    if (last) mma_commit(bar(C::B_OFULL + x));
+                  }
+                }
+              }
+              if (!ok) break;
+              pbit ^= bit;
+              if (last) obit ^= bit;
+            }
           }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        if (leader) {
+          if (v >= 0) mma_commit(bar(C::B_KVEMPTY + v));
+          if (k >= 0) mma_commit(bar(C::B_KVEMPTY + k));
+          if (k >= 0 && nj == u1 - 1) mma_commit(bar(C::B_QEMPTY + qs));
+        }
+        __syncwarp();
+        j = nj;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          cb0[x] = nb0[x];
+          cb1[x] = nb1[x];
         }
       }
     } else if (warp == 2) {
@@ -413,9 +471,12 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t my_s = tmem + lane_off + C::COL_S + 128 * x;
     const uint32_t my_o = tmem + lane_off + C::COL_O + DH * x;
-    const uint32_t ostg = base + C::OFF_OSTG + (uint32_t)(warp - 4) * C::OSTG_WARP;
     const int tk = row / a.vgroup, hd = row - tk * a.vgroup;
-    const float c2 = a.scale_log2, ca = c2 == 0.f ? 1.f : fabsf(c2);
+    // |scale| (S holds the products of -Q for a negative one); of a zero scale so little is kept that
+    // every logit is 0 and a masked one still -inf
+    const float c2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
+    const float2 c2v = make_float2(c2, c2);
+    const uint32_t my_p = tmem + lane_off + C::COL_P + C::P_STEP * x;
     uint32_t sc = 0, oc = 0;
     int64_t left = count;
     bool ok = true;
@@ -429,80 +490,86 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int tokens = x ? v.tok[1] : v.tok[0];
       if (tokens <= 0) continue;
       const int j0 = x ? v.b0[1] : v.b0[0], j1 = x ? v.b1[1] : v.b1[0];
-      const int pos = v.pos0 + x * a.rt1 + tk;
+      const int kvh = v.vhead / a.vheads, part = v.vhead - kvh * a.vheads;
+      const int head0 = kvh * a.group + part * a.vgroup;
+      const int nh = min(a.vgroup, a.group - part * a.vgroup);
+      const bool store = tk < tokens && hd < nh;
       const bool dead = quad * 32 >= tokens * a.vgroup;       // no row of this warp is stored
-      float m_run = -INFINITY, l_run = 0.f;
+      // the row sees the positions [low, pos]; the whole warp sees [wlow, wpos]
+      const int pos = v.pos0 + x * a.rt1 + tk;
+      const int low = (int)max((int64_t)pos - window + 1, (int64_t)0);
+      const int wpos = __reduce_min_sync(0xffffffffu, store ? pos : INT_MAX);
+      const int wlow = __reduce_max_sync(0xffffffffu, store ? low : 0);
+      float m_run = 0.f, l_run = 0.f;
       for (int j = j0; j < j1; ++j, ++sc) {
-        const bool w = mbar_wait(bar(C::B_SFULL + x), sc & 1u, abort_flag, kChunkTimeoutNs);
-        ok = __all_sync(0xffffffffu, w);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_SFULL + x), sc & 1u, abort_flag, kChunkTimeoutNs));
         if (!ok) break;
         tc_fence_after();
-        if (!dead) {
-          uint32_t s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tmem_ld_x32(my_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+        // P_x is rewritten, and O_x rescaled, once PV_x(j-1) is done
+        auto wait_pv = [&]() -> bool {
+          if (!C::EARLY || sc == 0) return true;
+          const bool w = mbar_wait(bar(C::B_PFREE + x), (sc - 1) & 1u, abort_flag, kChunkTimeoutNs);
+          tc_fence_after();
+          return __all_sync(0xffffffffu, w);
+        };
+        if (dead) {                              // (waits as the others do: none arrives a block ahead of them)
+          tc_fence_before();
+          __syncwarp();
+          if (C::EARLY && lane == 0) mbar_arrive(bar(C::B_SFREE + x));
+          ok = wait_pv();
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive(bar(C::B_PFULL + 2 * x));
+            mbar_arrive(bar(C::B_PFULL + 2 * x + 1));
+          }
+          continue;
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t s[64];
+          tmem_ld_x32(my_s + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+          tmem_ld_x32(my_s + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
           tmem_wait_ld();
-          // columns [clo, chi] of this block lie in the row's window; the others become -inf
-          // after the scale (whose sign may be either)
-          const int key0 = j << kBNTShift;
-          const int64_t lo = (int64_t)pos - window + 1 - key0;
-          const int clo = lo > 0 ? (int)min(lo, (int64_t)kBNT) : 0;
-          const int chi = min(kBNT - 1, pos - key0);
-          const bool neg = c2 < 0.f;
-          if (c2 == 0.f) {                        // (0 times a masked -inf would be NaN)
-#pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = 0u;
+          if (C::EARLY && h == 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(C::B_SFREE + x));    // S_x may be overwritten now
           }
-          if (__any_sync(0xffffffffu, clo > 0 || chi < kBNT - 1)) {
-            const uint32_t fill = __float_as_uint(neg ? INFINITY : -INFINITY);
+          const int key0 = (j << kBNTShift) + 64 * h;
+          if (key0 < wlow || wpos - key0 < 63) {                // positions outside [low, pos]
+            const int clo = low - key0, chi = pos - key0;
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] = i >= clo && i <= chi ? s[i] : fill;
-          }
-          if (neg) {
-#pragma unroll
-            for (int i = 0; i < 128; ++i) s[i] ^= 0x80000000u;
+            for (int i = 0; i < 64; ++i)
+              s[i] = i >= clo && i <= chi ? s[i] : __float_as_uint(-INFINITY);
           }
           float e4[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) e4[u] = __uint_as_float(s[u]);
 #pragma unroll
-          for (int i = 4; i < 124; i += 8)
+          for (int i = 4; i < 60; i += 8)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               e4[u] = max3(e4[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
 #pragma unroll
-          for (int u = 0; u < 4; ++u) e4[u] = fmaxf(e4[u], __uint_as_float(s[124 + u]));
-          const float top = max3(fmaxf(e4[0], e4[1]), e4[2], e4[3]);
-          const float m_blk = top * ca;
-          // the offset moves only when the maximum grew by more than 2^8
-          float alpha = 1.f;
-          bool move = false;
-          if (j == j0) {
-            m_run = m_blk;
-          } else if (m_blk > m_run + 8.f) {
-            alpha = ex2_approx(m_run - m_blk);
-            m_run = m_blk;
-            move = true;
+          for (int u = 0; u < 4; ++u) e4[u] = fmaxf(e4[u], __uint_as_float(s[60 + u]));
+          const float top = max3(fmaxf(e4[0], e4[1]), e4[2], e4[3]) * c2;
+          if (l_run == 0.f) {
+            if (top != -INFINITY) m_run = top;
           }
-          const float mo = m_run == -INFINITY ? 0.f : -m_run;
-          const float2 cav = make_float2(ca, ca), negm = make_float2(mo, mo);
-          float2 acc[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) acc[u] = make_float2(0.f, 0.f);
-          uint32_t pk[64];
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float2 y = __ffma2_rn(
-                make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), cav, negm);
-            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            acc[i & 3] = __fadd2_rn(acc[i & 3], e);
-            pk[i] = pack_bf16x2(e.x, e.y);
-          }
-          const float2 r = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-          l_run = l_run * alpha + (r.x + r.y);
-          if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
+          const bool move = l_run != 0.f && top > m_run + 8.f;
+          if (__any_sync(0xffffffffu, store && move)) {
+            if (h == 0) {
+              ok = wait_pv();
+            } else {                             // the product of this block's first half is under way
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait(bar(C::B_PHALF + x), sc & 1u, abort_flag, kChunkTimeoutNs));
+              tc_fence_after();
+            }
+            if (!ok) break;
+            const float alpha = move ? ex2_approx(m_run - top) : 1.f;
+            if (move) m_run = top;
+            l_run *= alpha;
+#pragma unroll 1
             for (int c = 0; c < DH; c += 16) {
               uint32_t ov[16];
               tmem_ld_x16(my_o + c, ov);
@@ -512,12 +579,32 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
               tmem_st_x16(my_o + c, ov);
             }
           }
-          tmem_st_x32(my_s, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-          tmem_st_x32(my_s + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          const float2 negm = make_float2(-m_run, -m_run);
+          float2 acc[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) acc[u] = make_float2(0.f, 0.f);
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float2 y = __ffma2_rn(
+                make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2v, negm);
+            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            acc[i & 3] = __fadd2_rn(acc[i & 3], e);
+            pk[i] = pack_bf16x2(e.x, e.y);
+          }
+          const float2 r = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l_run += r.x + r.y;
+          if (h == 0) {
+            ok = wait_pv();
+            if (!ok) break;
+          }
+          tmem_st_x32(my_p + 32 * h, pk);
           tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::B_PFULL + 2 * x + h));
         }
-        tc_fence_before();
-        mbar_arrive(bar(C::B_PFULL + x));
+        if (!ok) break;
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
@@ -529,9 +616,6 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         ++oc;
         tc_fence_after();
       }
-      const int kvh = v.vhead / a.vheads, part = v.vhead - kvh * a.vheads;
-      const int head0 = kvh * a.group + part * a.vgroup;
-      const int nh = min(a.vgroup, a.group - part * a.vgroup);
       const bool whole = (v.flags & kBegins) && (v.flags & kEnds);
       const int64_t at = 2 * worker + ((v.flags & kBegins) ? 1 : 0);
       if (!whole && x == 0 && threadIdx.x == 128) {
@@ -543,89 +627,52 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         pc.ends = (v.flags & kEnds) ? 1 : 0;
         a.piece[at] = pc;
       }
-      const bool store = tk < tokens && hd < nh;
-      if (dead) {
-        if (has_o) {
-          tc_fence_before();
-          mbar_arrive(bar(C::B_OEMPTY + x));
-        }
-        continue;
-      }
-      if (!whole) {
-        const int pr = x * 128 + row;
-        float* dst = a.po + at * a.rows * DH + pr * 4;
-        if (store) a.ml[at * a.rows + pr] = make_float2(m_run, l_run);
-        if (has_o) {
-#pragma unroll
-          for (int c = 0; c < DH; c += 16) {
-            uint32_t ov[16];
-            tmem_ld_x16(my_o + c, ov);
-            tmem_wait_ld();
-            if (store)
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<uint4*>(dst + (int64_t)((c + i) / 4) * a.rows * 4) =
-                    make_uint4(ov[i], ov[i + 1], ov[i + 2], ov[i + 3]);
-          }
-          tc_fence_before();
-          mbar_arrive(bar(C::B_OEMPTY + x));
-        }
-        continue;
-      }
-      const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
-      if (a.lse && store)
-        a.lse[(int64_t)(head0 + hd) * a.T + v.token0 + x * a.rt1 + tk] =
-            l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
-      // rows pass through this warp's staging area (16-byte units swizzled by row), so
-      // that a store instruction writes whole rows
-      constexpr int PC = DH < 64 ? DH : 64, CPR = PC / 8, RPI = 32 / CPR;
-      auto unit = [&](int r, int u) -> uint32_t {
-        const int sw = CPR == 8 ? (r & 7) : ((r >> 1) & 3);
-        return ostg + (uint32_t)(r * CPR * 16) + ((uint32_t)(u ^ sw) << 4);
+      auto free_o = [&]() {                      // the O accumulator is read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_OEMPTY + x));
       };
-#pragma unroll
-      for (int c0 = 0; c0 < DH; c0 += PC) {
-        uint32_t o[PC];
+      if (dead) {
+        if (has_o) free_o();
+        continue;
+      }
+      // a whole row of O is normalised and stored by its thread, 32 bytes (one sector) at a time;
+      // a row of a piece goes to the workspace as it is
+      const int pr = x * 128 + row;
+      const int64_t t = v.token0 + x * a.rt1 + tk;
+      const float inv = l_run > 0.f || l_run != l_run ? 1.f / l_run : 0.f;
+      if (store && whole && a.lse)
+        a.lse[(int64_t)(head0 + hd) * a.T + t] =
+            l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * 0.69314718055994531f;
+      if (store && !whole) a.ml[at * a.rows + pr] = make_float2(m_run, l_run);
+      __nv_bfloat16* o = a.o + (t * a.hq + head0 + hd) * DH;
+      float* po = a.po + at * a.rows * DH + pr * 4;
+#pragma unroll 1
+      for (int c = 0; c < DH; c += 16) {
+        uint32_t ov[16];
         if (has_o) {
-#pragma unroll
-          for (int c = 0; c < PC; c += 16)
-            tmem_ld_x16(my_o + c0 + c, *reinterpret_cast<uint32_t(*)[16]>(&o[c]));
+          tmem_ld_x16(my_o + c, ov);
           tmem_wait_ld();
-          if (c0 + PC == DH) {
-            tc_fence_before();
-            mbar_arrive(bar(C::B_OEMPTY + x));
-          }
         } else {
 #pragma unroll
-          for (int c = 0; c < PC; ++c) o[c] = 0u;
+          for (int i = 0; i < 16; ++i) ov[i] = 0u;
         }
+        if (store && whole) {
+          uint32_t p[8];
 #pragma unroll
-        for (int u = 0; u < CPR; ++u) {
-          uint32_t p[4];
+          for (int i = 0; i < 8; ++i)
+            p[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+          reinterpret_cast<uint4*>(o + c)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+          reinterpret_cast<uint4*>(o + c)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+        } else if (store) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            p[i] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * i]) * inv,
-                               __uint_as_float(o[8 * u + 2 * i + 1]) * inv);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(unit(lane, u)), "r"(p[0]),
-                       "r"(p[1]), "r"(p[2]), "r"(p[3])
-                       : "memory");
-        }
-        __syncwarp();
-        const int rl = lane / CPR, ul = lane % CPR;
-#pragma unroll
-        for (int it = 0; it < CPR; ++it) {
-          const int r = it * RPI + rl, tr = quad * 32 + r;
-          const int t = tr / a.vgroup, h = tr - t * a.vgroup;
-          uint4 val;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(val.x), "=r"(val.y), "=r"(val.z), "=r"(val.w)
-                       : "r"(unit(r, ul)));
-          if (t < tokens && h < nh)
-            *reinterpret_cast<uint4*>(a.o + ((int64_t)(v.token0 + x * a.rt1 + t) * a.hq + head0 + h) * DH +
-                                      c0 + ul * 8) = val;
+            *reinterpret_cast<uint4*>(po + (int64_t)(c / 4 + i) * a.rows * 4) =
+                make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
         }
         __syncwarp();
       }
+      if (has_o) free_o();
     }
   }
 
@@ -634,7 +681,7 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   if (*abort_flag) {
     volatile int never = 0;
-    if (warp == 1 && lane == 0) {
+    if ((warp == 1 || (C::EARLY && warp == 3)) && elect_one()) {
       mma_commit(bar(C::B_DRAIN));                       // all MMAs issued so far
       mbar_wait(bar(C::B_DRAIN), 0, &never, kChunkTimeoutNs);
     }
