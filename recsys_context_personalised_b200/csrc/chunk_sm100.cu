@@ -15,25 +15,22 @@
 //
 // CTA = 12 warps, one per SM:
 //   warp 0      TMA producer: Q of a visit (a run of one item's blocks), K and V page by page
-//   warp 1      MMA issuer (one lane); dh <= 64: of tile A, and warp 3 of tile B
+//   warp 1      MMA issuer: per block PV_A(j), S_A(j+1), PV_B(j), S_B(j+1)
 //   warp 2      TMEM allocator; zeroes the V rows of an item's first and last block
 //               that no row of the item sees (0 * NaN would reach O through the product)
 //   warps 4-7   softmax of tile A, warps 8-11 of tile B (thread = row = TMEM lane)
 //
-// TMEM columns: S_A [0,128), S_B [128,256), O_A [256, 256+dh), O_B [256+dh, 256+2dh).  dh <= 64:
-// P_X (packed bf16) at [384 + 64X, 448 + 64X), and S_X(j+1) is issued as soon as S_X(j) lies in
-// registers (EARLY).  dh = 128: P_X aliases the first 64 columns of S_X, so S_X(j+1) is issued
-// behind PV_X(j).  P goes out in two halves of 64 keys; the product of the
-// first half runs while the second is computed.
+// TMEM columns: S_A [0,128), S_B [128,256), O_A [256, 256+dh), O_B [256+dh, 256+2dh).  P_X (packed
+// bf16) aliases the first 64 columns of S_X, so S_X(j+1) is issued behind PV_X(j).  P goes out in two
+// halves of 64 keys; the product of the first runs while the second is computed.
 //
-// Softmax: online, 64 keys at a time, the running offset kept while a half's maximum stays
-// within 2^8 of it (softmax does not depend on the offset, and 2^8 is far from overflow).
-// P is rounded to bf16, the precision of the MMA's operand; its sum l is taken before that.
+// Softmax: online, the running offset kept while a block's maximum stays within 2^8 of it
+// (softmax does not depend on the offset, and 2^8 is far from overflow).  P is rounded to
+// bf16, the precision of the MMA's operand; its sum l is taken before that.
 //
-// The code is kept short on purpose (rolled loops over halves and column groups): a launch
-// fetches it cold, and with both halves, the masked and the unmasked path and the tiles unrolled
-// the warps waited for instructions most of the time on short windows (0.28 ms for 48
-// sessions of up to 700 events in a 256-event window).
+// The code is kept short and its rare parts out of line: a launch fetches it cold, and the warps
+// waited for instructions most of the time with separate masked and unmasked paths
+// (0.28 ms for 48 sessions of up to 700 events in a 256-event window, against 0.14 ms).
 #include <limits.h>
 #include <math.h>
 
@@ -70,13 +67,10 @@ struct CfgT {
   static constexpr int NS = DH == 32 ? 16 : DH == 64 ? 10 : 5;   // K/V ring slots
   static constexpr int NV = 8;                          // barriers of V blocks that pass warp 2
   static_assert((NS + 1) / 2 <= NV, "as many as V blocks in flight");
-  static constexpr bool EARLY = DH <= 64;               // P has columns of its own
-  static constexpr int NI = EARLY ? 2 : 1;              // MMA issuers
-  static constexpr uint32_t COL_S = 0, COL_O = 256, COL_P = EARLY ? 384 : 0, P_STEP = EARLY ? 64 : 128;
-  // SFREE: S read; PHALF: the product with P's first half done, PFREE: with all of P
-  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_SFREE = 6, B_PFULL = 8, B_PHALF = 12,
-                       B_PFREE = 14, B_OFULL = 16, B_OEMPTY = 18, B_DRAIN = 20, B_VRAW = 21,
-                       B_KVFULL = B_VRAW + NV, B_KVEMPTY = B_KVFULL + NS, NBAR = B_KVEMPTY + NS;
+  static constexpr uint32_t COL_S = 0, COL_O = 256;
+  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 10, B_OEMPTY = 12,
+                       B_DRAIN = 14, B_VRAW = 15, B_KVFULL = B_VRAW + NV, B_KVEMPTY = B_KVFULL + NS,
+                       NBAR = B_KVEMPTY + NS;
   static constexpr uint32_t OFF_Q = 0, OFF_KV = QST * 2 * TILEB, OFF_CTL = OFF_KV + NS * TILEB;
   static constexpr uint32_t CTL_TMEM = 8 * NBAR, CTL_ABORT = CTL_TMEM + 4,
                             CTL_VISIT = (CTL_ABORT + 4 + 15) / 16 * 16,
@@ -94,6 +88,32 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r));
   return r != 0;
+}
+
+// The products and commits of a converged warp, issued by the elected lane under a predicate (not on
+// a branch of its own, so that the operands stay in uniform registers).
+__device__ __forceinline__ void mma_ss_if(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 l, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}" ::"r"(on), "r"(d), "l"(a),
+      "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 l, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}" ::"r"(on), "r"(d), "r"(a),
+      "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %0, 0;\n\t"
+      "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(on),
+      "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -129,21 +149,18 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_QFULL + i), 1);
-      mbar_init(bar(C::B_QEMPTY + i), 9 + C::NI);   // the MMA issuers, warp 2 and the 8 softmax warps
+      mbar_init(bar(C::B_QEMPTY + i), 10);     // the MMA issuer, warp 2 and the 8 softmax warps
       mbar_init(bar(C::B_SFULL + i), 1);
-      mbar_init(bar(C::B_SFREE + i), 4);
       mbar_init(bar(C::B_PFULL + i), 4);
       mbar_init(bar(C::B_PFULL + 2 + i), 4);
-      mbar_init(bar(C::B_PHALF + i), 1);
-      mbar_init(bar(C::B_PFREE + i), 1);
       mbar_init(bar(C::B_OFULL + i), 1);
       mbar_init(bar(C::B_OEMPTY + i), 4);
     }
-    mbar_init(bar(C::B_DRAIN), C::NI);
+    mbar_init(bar(C::B_DRAIN), 1);
     for (int i = 0; i < C::NV; ++i) mbar_init(bar(C::B_VRAW + i), 1);
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(bar(C::B_KVFULL + i), 1);
-      mbar_init(bar(C::B_KVEMPTY + i), C::NI);
+      mbar_init(bar(C::B_KVEMPTY + i), 1);
     }
     *abort_flag = 0;
     bad_page = 0;
@@ -303,20 +320,17 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           }
         }
       }
-    } else if (warp == 1 || (C::EARLY && warp == 3)) {
-      // ------------------------------------------------------- MMA issuers
-      // Both tiles in one in-order stream, PV_A(j), S_A(j+1), PV_B(j), S_B(j+1); or (EARLY) a
-      // stream of its own for each tile, S_X(j+1), PV_X(j).  The whole warp walks the blocks and
-      // one elected lane issues: values that are the same in the warp (as a broadcast tells the compiler)
-      // stay in uniform registers, where the descriptors have to be; issued by a lane on its
-      // own branch a product took 85 to 100 cycles to issue.
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      // Both tiles in one in-order stream, PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).  The whole warp walks the blocks and
+      // one elected lane issues under a predicate: values that are the same in the warp (as a
+      // broadcast tells the compiler) stay in uniform registers, where the descriptors have to be.
       auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
       const uint32_t tm = (uint32_t)uni((int)tmem);
-      const bool leader = elect_one();
-      const int x_lo = C::EARLY && uni(warp) == 3 ? 1 : 0, x_hi = C::EARLY ? x_lo : 1;
+      const uint32_t leader = elect_one();
       // a negative scale: the products of -Q, and its absolute value in the softmax
       const uint32_t idesc_s = IDESC_S | (a.scale_log2 < 0.f ? 1u << 13 : 0u);
-      uint32_t slot = 0, phase = 0, vn = 0, qs = 0, scnt = 0, pbit = 0, obit = 0;
+      uint32_t slot = 0, phase = 0, vn = 0, qs = 0, pbit = 0, obit = 0;
       auto wait = [&](int b, uint32_t parity) -> bool {
         const bool w = __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kChunkTimeoutNs));
         tc_fence_after();
@@ -356,66 +370,45 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         }
         if (!ok) break;
 #pragma unroll 1
-        for (int x = x_lo; x <= x_hi; ++x) {
+        for (int x = 0; ok && x < 2; ++x) {
           const int c0 = x ? cb0[1] : cb0[0], c1 = x ? cb1[1] : cb1[0];
           const int n0 = x ? nb0[1] : nb0[0], n1 = x ? nb1[1] : nb1[0];
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            if ((half == 0) == C::EARLY) {                    // S_X(nj)
-              if (k < 0 || nj < n0 || nj >= n1) continue;
-              if (C::EARLY) {
-                if (scnt > 0) ok = wait(C::B_SFREE + x, (scnt - 1) & 1u);
-                if (!ok) break;
-                ++scnt;
-              }
-              const uint64_t a0 = smem_desc(sQ + (qs * 2 + x) * C::TILEB, 16, C::ATOM, C::SW);
-              const uint64_t b0 = smem_desc(sKV + k * C::TILEB, 16, C::ATOM, C::SW);
-              if (leader) {
+          if (v >= 0 && j >= c0 && j < c1) {                  // O_X += P_X(j) V(j)
+            const bool first = j == c0, last = j == c1 - 1;
+            const uint64_t v0 = smem_desc(sKV + v * C::TILEB, C::CHUNKB, C::ATOM, C::SW);
 #pragma unroll
-                for (int q = 0; q < DH / 16; ++q) {
-                  const uint32_t off = (q / (C::CH / 16)) * C::CHUNKB + (q % (C::CH / 16)) * 32;
-                  mma_ss(tm + C::COL_S + 128 * x, desc_advance(a0, off), desc_advance(b0, off), idesc_s,
-                         q > 0 ? 1u : 0u);
-                }
-                mma_commit(bar(C::B_SFULL + x));
-              }
-            } else {                                          // O_X += P_X(j) V(j)
-              if (v < 0 || j < c0 || j >= c1) continue;
-              const uint32_t bit = 1u << x;
-              const bool first = j == c0, last = j == c1 - 1;
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                ok = wait(C::B_PFULL + 2 * x + h, (pbit >> x) & 1u);
-                if (ok && h == 0 && first) ok = wait(C::B_OEMPTY + x, ((obit >> x) & 1u) ^ 1u);
-                if (!ok) break;
-                const uint64_t v0 = desc_advance(smem_desc(sKV + v * C::TILEB, C::CHUNKB, C::ATOM, C::SW),
-                                                 h * 8 * C::ATOM);
-                if (leader) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q)
-                    mma_ts(tm + C::COL_O + DH * x, tm + C::COL_P + C::P_STEP * x + h * 32 + q * 8,
-                           desc_advance(v0, q * 2 * C::ATOM), IDESC_O, q > 0 || h > 0 || !first ? 1u : 0u);
-                  if (h == 0) {
-                    mma_commit(bar(C::B_PHALF + x));
-                  } else {
-                    if (C::EARLY) mma_commit(bar(C::B_PFREE + x));
-                    if (last) mma_commit(bar(C::B_OFULL + x));
-                  }
-                }
-              }
+            for (int h = 0; h < 2; ++h) {
+              ok = wait(C::B_PFULL + 2 * x + h, (pbit >> x) & 1u);
+              if (ok && h == 0 && first) ok = wait(C::B_OEMPTY + x, ((obit >> x) & 1u) ^ 1u);
               if (!ok) break;
-              pbit ^= bit;
-              if (last) obit ^= bit;
+#pragma unroll
+              for (int q = 4 * h; q < 4 * h + 4; ++q)
+                mma_ts_if(leader, tm + C::COL_O + DH * x, tm + C::COL_S + 128 * x + q * 8,
+                          desc_advance(v0, q * 2 * C::ATOM), IDESC_O, q > 0 || !first ? 1u : 0u);
+            }
+            if (!ok) break;
+            pbit ^= 1u << x;
+            if (last) {
+              commit_if(leader, bar(C::B_OFULL + x));
+              obit ^= 1u << x;
             }
           }
-          if (!ok) break;
+          if (k >= 0 && nj >= n0 && nj < n1) {                // S_X(nj)
+            const uint64_t a0 = smem_desc(sQ + (qs * 2 + x) * C::TILEB, 16, C::ATOM, C::SW);
+            const uint64_t b0 = smem_desc(sKV + k * C::TILEB, 16, C::ATOM, C::SW);
+#pragma unroll
+            for (int q = 0; q < DH / 16; ++q) {
+              const uint32_t off = (q / (C::CH / 16)) * C::CHUNKB + (q % (C::CH / 16)) * 32;
+              mma_ss_if(leader, tm + C::COL_S + 128 * x, desc_advance(a0, off), desc_advance(b0, off),
+                        idesc_s, q > 0 ? 1u : 0u);
+            }
+            commit_if(leader, bar(C::B_SFULL + x));
+          }
         }
         if (!ok) break;
-        if (leader) {
-          if (v >= 0) mma_commit(bar(C::B_KVEMPTY + v));
-          if (k >= 0) mma_commit(bar(C::B_KVEMPTY + k));
-          if (k >= 0 && nj == u1 - 1) mma_commit(bar(C::B_QEMPTY + qs));
-        }
+        if (v >= 0) commit_if(leader, bar(C::B_KVEMPTY + v));
+        if (k >= 0) commit_if(leader, bar(C::B_KVEMPTY + k));
+        if (k >= 0 && nj == u1 - 1) commit_if(leader, bar(C::B_QEMPTY + qs));
         __syncwarp();
         j = nj;
 #pragma unroll
@@ -476,7 +469,6 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // every logit is 0 and a masked one still -inf
     const float c2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
     const float2 c2v = make_float2(c2, c2);
-    const uint32_t my_p = tmem + lane_off + C::COL_P + C::P_STEP * x;
     uint32_t sc = 0, oc = 0;
     int64_t left = count;
     bool ok = true;
@@ -505,105 +497,81 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         ok = __all_sync(0xffffffffu, mbar_wait(bar(C::B_SFULL + x), sc & 1u, abort_flag, kChunkTimeoutNs));
         if (!ok) break;
         tc_fence_after();
-        // P_x is rewritten, and O_x rescaled, once PV_x(j-1) is done
-        auto wait_pv = [&]() -> bool {
-          if (!C::EARLY || sc == 0) return true;
-          const bool w = mbar_wait(bar(C::B_PFREE + x), (sc - 1) & 1u, abort_flag, kChunkTimeoutNs);
-          tc_fence_after();
-          return __all_sync(0xffffffffu, w);
-        };
-        if (dead) {                              // (waits as the others do: none arrives a block ahead of them)
+        // (PV_x(j-1), which reads P_x and writes O_x, is done: S_x(j) came behind it)
+        if (dead) {
           tc_fence_before();
           __syncwarp();
-          if (C::EARLY && lane == 0) mbar_arrive(bar(C::B_SFREE + x));
-          ok = wait_pv();
-          if (!ok) break;
           if (lane == 0) {
             mbar_arrive(bar(C::B_PFULL + 2 * x));
             mbar_arrive(bar(C::B_PFULL + 2 * x + 1));
           }
           continue;
         }
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s[64];
-          tmem_ld_x32(my_s + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-          tmem_ld_x32(my_s + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[32]));
-          tmem_wait_ld();
-          if (C::EARLY && h == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(C::B_SFREE + x));    // S_x may be overwritten now
-          }
-          const int key0 = (j << kBNTShift) + 64 * h;
-          if (key0 < wlow || wpos - key0 < 63) {                // positions outside [low, pos]
-            const int clo = low - key0, chi = pos - key0;
+        uint32_t s[128];
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              s[i] = i >= clo && i <= chi ? s[i] : __float_as_uint(-INFINITY);
-          }
-          float e4[4];
+        for (int c = 0; c < 4; ++c)
+          tmem_ld_x32(my_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+        tmem_wait_ld();
+        const int key0 = j << kBNTShift;
+        if (__builtin_expect(key0 < wlow || wpos - key0 < kBNT - 1, 0)) {   // positions outside [low, pos]
+          const int clo = low - key0, chi = pos - key0;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) e4[u] = __uint_as_float(s[u]);
+          for (int i = 0; i < 128; ++i)
+            s[i] = i >= clo && i <= chi ? s[i] : __float_as_uint(-INFINITY);
+        }
+        float e4[4];
 #pragma unroll
-          for (int i = 4; i < 60; i += 8)
+        for (int u = 0; u < 4; ++u) e4[u] = __uint_as_float(s[u]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              e4[u] = max3(e4[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+        for (int i = 4; i < 124; i += 8)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) e4[u] = fmaxf(e4[u], __uint_as_float(s[60 + u]));
-          const float top = max3(fmaxf(e4[0], e4[1]), e4[2], e4[3]) * c2;
-          if (l_run == 0.f) {
-            if (top != -INFINITY) m_run = top;
-          }
-          const bool move = l_run != 0.f && top > m_run + 8.f;
-          if (__any_sync(0xffffffffu, store && move)) {
-            if (h == 0) {
-              ok = wait_pv();
-            } else {                             // the product of this block's first half is under way
-              ok = __all_sync(0xffffffffu,
-                              mbar_wait(bar(C::B_PHALF + x), sc & 1u, abort_flag, kChunkTimeoutNs));
-              tc_fence_after();
-            }
-            if (!ok) break;
-            const float alpha = move ? ex2_approx(m_run - top) : 1.f;
-            if (move) m_run = top;
-            l_run *= alpha;
+          for (int u = 0; u < 4; ++u)
+            e4[u] = max3(e4[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e4[u] = fmaxf(e4[u], __uint_as_float(s[124 + u]));
+        const float top = max3(fmaxf(e4[0], e4[1]), e4[2], e4[3]) * c2;
+        // a first visible key (l = 0) sets the offset, a maximum beyond 2^8 of it moves it
+        const bool move = l_run == 0.f ? top != -INFINITY : top > m_run + 8.f;
+        if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
+          const float alpha = move ? ex2_approx(m_run - top) : 1.f;
+          if (move) m_run = top;
+          if (__any_sync(0xffffffffu, move && l_run != 0.f)) {
+            const float f = l_run != 0.f ? alpha : 0.f;
+            l_run *= f;
 #pragma unroll 1
             for (int c = 0; c < DH; c += 16) {
               uint32_t ov[16];
               tmem_ld_x16(my_o + c, ov);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
               tmem_st_x16(my_o + c, ov);
             }
           }
-          const float2 negm = make_float2(-m_run, -m_run);
-          float2 acc[4];
+        }
+        const float2 negm = make_float2(-m_run, -m_run);
+        float2 acc[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) acc[u] = make_float2(0.f, 0.f);
+        for (int u = 0; u < 4; ++u) acc[u] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           uint32_t pk[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float2 y = __ffma2_rn(
-                make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2v, negm);
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[64 * h + 2 * i]),
+                                                    __uint_as_float(s[64 * h + 2 * i + 1])), c2v, negm);
             const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             acc[i & 3] = __fadd2_rn(acc[i & 3], e);
             pk[i] = pack_bf16x2(e.x, e.y);
           }
-          const float2 r = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-          l_run += r.x + r.y;
-          if (h == 0) {
-            ok = wait_pv();
-            if (!ok) break;
-          }
-          tmem_st_x32(my_p + 32 * h, pk);
+          tmem_st_x32(my_s + 32 * h, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::B_PFULL + 2 * x + h));
         }
+        const float2 r = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        l_run += r.x + r.y;
         if (!ok) break;
       }
       if (!ok) break;
@@ -681,7 +649,7 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   __syncthreads();
   if (*abort_flag) {
     volatile int never = 0;
-    if ((warp == 1 || (C::EARLY && warp == 3)) && elect_one()) {
+    if (warp == 1 && elect_one()) {
       mma_commit(bar(C::B_DRAIN));                       // all MMAs issued so far
       mbar_wait(bar(C::B_DRAIN), 0, &never, kChunkTimeoutNs);
     }
