@@ -126,6 +126,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   }
   if (threadIdx.x < 2) a.piece[2 * worker + threadIdx.x].tokens = 0;
   find_start(a, worker, &start, scan);            // (synchronises the block)
+  pdl_trigger();
   const int64_t count = start.count;
 
   if (warp == kWarps) {
@@ -539,18 +540,34 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                                    : start.bad || bad_page ? GDPA_ERR_INVALID_ARG : GDPA_OK;
 }
 
+struct Partial {                                              // of one row and 4 columns
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ void merge(Partial& a, const float2 ml, const float4 v) {
+  if (ml.y == 0.f) return;                                    // a piece that this row sees nothing of
+  const float top = fmaxf(a.m, ml.x);
+  const float f = sm100::ex2_approx(a.m - top), g = sm100::ex2_approx(ml.x - top);
+  a.m = top;
+  a.l = a.l * f + ml.y * g;
+  a.o.x = a.o.x * f + v.x * g;
+  a.o.y = a.o.y * f + v.y * g;
+  a.o.z = a.o.z * f + v.z * g;
+  a.o.w = a.o.w * f + v.w * g;
+}
+
 // Joins the pieces of the item that begins in worker blockIdx.x's part and ends
-// in a later one: 8 rows at a time, a warp to 16 columns of every SPLIT-th piece, pieces merged
-// in the workers' order, then the splits in theirs.
-constexpr int kJoinThreads = 512;
-template <int DH>
-__global__ void __launch_bounds__(kJoinThreads)
+// in a later one, 8 rows (blockIdx.y) to a block: a warp to 16 columns of every SPLIT-th
+// piece, merged in the workers' order, then the splits in theirs.
+template <int DH, int SPLIT>
+__global__ void __launch_bounds__(DH / 16 * SPLIT * 32)
 chunk_join_kernel(const ChunkArgs a, WsHeader* ws) {
-  constexpr int GROUPS = DH / 16, SPLIT = kJoinThreads / 32 / GROUPS;
+  constexpr int GROUPS = DH / 16;
   __shared__ float4 sacc[SPLIT][GROUPS][32];
   __shared__ float2 sml[SPLIT][GROUPS][8];
   __shared__ int worst;
   const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
   if (w == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) worst = 0;
     __syncthreads();
@@ -560,7 +577,11 @@ chunk_join_kernel(const ChunkArgs a, WsHeader* ws) {
     if (threadIdx.x == 0) ws->status = worst;
   }
   const ChunkPiece first = a.piece[2 * w + 1];
-  if (first.tokens == 0) return;
+  const int cg = warp % GROUPS, sp = warp / GROUPS, r8 = lane & 7, c4 = lane >> 3;
+  const int r = blockIdx.y * 8 + r8, x = r / a.tile_rows, rr = r - x * a.tile_rows;
+  const int tk = rr / a.vgroup, h = rr - tk * a.vgroup;
+  const bool live = tk < a.rt1 && x * a.rt1 + tk < first.tokens && h < first.heads;
+  if (!__any_sync(0xffffffffu, live)) return;                 // (the same in every warp of the block)
   // worker of the item's last piece: the next one that holds the item's end
   int last = w + 1;
   for (; last < a.workers; last += 32) {
@@ -573,61 +594,45 @@ chunk_join_kernel(const ChunkArgs a, WsHeader* ws) {
     }
   }
   last = min(last, a.workers - 1);
-  const int cg = warp % GROUPS, sp = warp / GROUPS, r8 = lane & 7, c4 = lane >> 3;
-  for (int r0 = blockIdx.y * 8; r0 < a.rows; r0 += gridDim.y * 8) {
-    const int r = r0 + r8, x = r / a.tile_rows, rr = r - x * a.tile_rows;
-    const int tk = rr / a.vgroup, h = rr - tk * a.vgroup;
-    const bool live = tk < a.rt1 && x * a.rt1 + tk < first.tokens && h < first.heads;
-    if (__syncthreads_or(live) == 0) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-#pragma unroll 4
-      for (int i = w + sp; i <= last; i += SPLIT) {
-        const int64_t at = i == w ? 2 * w + 1 : 2 * i;
-        const float2 ml = a.ml[at * a.rows + r];
-        const float4 v = *reinterpret_cast<const float4*>(
-            a.po + at * a.rows * DH + ((int64_t)(cg * 4 + c4) * a.rows + r) * 4);
-        if (ml.y == 0.f) continue;                            // a piece that this row sees nothing of
-        const float top = fmaxf(m, ml.x);
-        const float f = sm100::ex2_approx(m - top), g = sm100::ex2_approx(ml.x - top);
-        m = top;
-        l = l * f + ml.y * g;
-        acc.x = acc.x * f + v.x * g;
-        acc.y = acc.y * f + v.y * g;
-        acc.z = acc.z * f + v.z * g;
-        acc.w = acc.w * f + v.w * g;
-      }
-      sacc[sp][cg][lane] = acc;
-      if (c4 == 0) sml[sp][cg][r8] = make_float2(m, l);
-    }
-    __syncthreads();
-    if (live && sp == 0) {
+  Partial p = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int64_t col = ((int64_t)(cg * 4 + c4) * a.rows + r) * 4;
+  if (live) {
+    constexpr int U = 4;
+    for (int i = w + sp; i <= last; i += U * SPLIT) {
+      float2 ml[U];
+      float4 v[U];
 #pragma unroll
-      for (int i = 1; i < SPLIT; ++i) {
-        const float2 ml = sml[i][cg][r8];
-        const float4 v = sacc[i][cg][lane];
-        if (ml.y == 0.f) continue;
-        const float top = fmaxf(m, ml.x);
-        const float f = sm100::ex2_approx(m - top), g = sm100::ex2_approx(ml.x - top);
-        m = top;
-        l = l * f + ml.y * g;
-        acc.x = acc.x * f + v.x * g;
-        acc.y = acc.y * f + v.y * g;
-        acc.z = acc.z * f + v.z * g;
-        acc.w = acc.w * f + v.w * g;
+      for (int u = 0; u < U; ++u) {
+        const int k = i + u * SPLIT;
+        const int64_t at = k == w ? 2 * w + 1 : 2 * k;
+        ml[u] = make_float2(0.f, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= last) {
+          ml[u] = a.ml[at * a.rows + r];
+          v[u] = *reinterpret_cast<const float4*>(a.po + at * a.rows * DH + col);
+        }
       }
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const int64_t t = first.token0 + x * a.rt1 + tk;
-      *reinterpret_cast<uint2*>(a.o + (t * a.hq + first.head0 + h) * DH + (cg * 4 + c4) * 4) =
-          make_uint2(sm100::pack_bf16x2(acc.x * inv, acc.y * inv),
-                     sm100::pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (a.lse && cg == 0 && c4 == 0)
-        a.lse[(int64_t)(first.head0 + h) * a.T + t] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) merge(p, ml[u], v[u]);
     }
-    __syncthreads();
   }
+  if constexpr (SPLIT > 1) {
+    sacc[sp][cg][lane] = p.o;
+    if (c4 == 0) sml[sp][cg][r8] = make_float2(p.m, p.l);
+    __syncthreads();
+    if (sp > 0) return;
+#pragma unroll
+    for (int i = 1; i < SPLIT; ++i) merge(p, sml[i][cg][r8], sacc[i][cg][lane]);
+  }
+  if (!live) return;
+  const float inv = p.l > 0.f || p.l != p.l ? 1.f / p.l : 0.f;
+  const int64_t t = first.token0 + x * a.rt1 + tk;
+  *reinterpret_cast<uint2*>(a.o + (t * a.hq + first.head0 + h) * DH + (cg * 4 + c4) * 4) =
+      make_uint2(sm100::pack_bf16x2(p.o.x * inv, p.o.y * inv),
+                 sm100::pack_bf16x2(p.o.z * inv, p.o.w * inv));
+  if (a.lse && cg == 0 && c4 == 0)
+    a.lse[(int64_t)(first.head0 + h) * a.T + t] =
+        p.l == 0.f ? -INFINITY : (p.m + log2f(p.l)) * 0.69314718055994531f;
 }
 
 template <int DH, int MT>
@@ -714,13 +719,27 @@ bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int b
          make(v, 4, c.v, size, stride, box);
 }
 
-cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st) {
+template <int DH, int SPLIT>
+cudaError_t launch_join(const ChunkArgs& a, WsHeader* ws, cudaStream_t st) {
   KernelScope ks_("gdpa_chunk_join", st);
-  const dim3 grid(a.workers, a.rows < 64 ? a.rows / 8 : 8);
-  if (dh == 32) chunk_join_kernel<32><<<grid, kJoinThreads, 0, st>>>(a, ws);
-  if (dh == 64) chunk_join_kernel<64><<<grid, kJoinThreads, 0, st>>>(a, ws);
-  if (dh == 128) chunk_join_kernel<128><<<grid, kJoinThreads, 0, st>>>(a, ws);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.workers, a.rows / 8);
+  cfg.blockDim = dim3(DH / 16 * SPLIT * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<DH, SPLIT>, a, ws);
+}
+cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st) {
+  // few items leave many pieces to each (about workers / items): 512 threads share them
+  const int64_t tiles = a.T / a.rt > a.B ? a.T / a.rt : a.B;
+  const bool many = tiles * a.hk * a.vheads * 8 < a.workers;
+  if (dh == 32) return many ? launch_join<32, 8>(a, ws, st) : launch_join<32, 1>(a, ws, st);
+  if (dh == 64) return many ? launch_join<64, 4>(a, ws, st) : launch_join<64, 1>(a, ws, st);
+  return many ? launch_join<128, 2>(a, ws, st) : launch_join<128, 1>(a, ws, st);
 }
 
 }  // namespace gdpa

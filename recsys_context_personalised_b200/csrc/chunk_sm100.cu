@@ -180,6 +180,7 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   const int64_t count = start.count;              // blocks of this worker
 
@@ -516,8 +517,15 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         if (__builtin_expect(key0 < wlow || wpos - key0 < kBNT - 1, 0)) {   // positions outside [low, pos]
           const int clo = low - key0, chi = pos - key0;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            s[i] = i >= clo && i <= chi ? s[i] : __float_as_uint(-INFINITY);
+          for (int w = 0; w < 4; ++w) {
+            // bits lo .. hi of a word (tests of constant bits cost half of two comparisons each)
+            const int lo = clo - 32 * w, hi = chi - 32 * w;
+            uint32_t m = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
+            m &= hi >= 31 ? 0xffffffffu : hi < 0 ? 0u : 0xffffffffu >> (31 - hi);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              s[32 * w + i] = (m >> i) & 1u ? s[32 * w + i] : __float_as_uint(-INFINITY);
+          }
         }
         float e4[4];
 #pragma unroll
