@@ -21,101 +21,10 @@
 #include <math.h>
 #include <stdio.h>
 
-#include "gdpa_internal.cuh"
+#include "block_norm.cuh"
 
 namespace gdpa {
 namespace {
-
-struct NormArgs {
-  const void *x, *f, *gate;      // backward: x is the forward's y
-  const float *w_post, *w_pre;
-  const int32_t* offsets;        // sample gates: [B + 1]
-  void *y, *n;                   // forward outputs
-  const void *dy, *dn;           // backward inputs
-  void *dx, *df, *dgate;         // backward outputs (dgate: token gates)
-  float* dgate_sample;           // [B, d] (sample gates)
-  float *part_post, *part_pre;   // [blocks, d] partial weight gradients
-  float* part_gate;              // [groups, 2, d] partial sample-gate gradients
-  int64_t T;
-  int d, B, groups;
-  float alpha, eps, inv_d;
-  int gate_kind, sigmoid;
-};
-
-__device__ __forceinline__ float logistic(float z) { return 1.f / (1.f + __expf(-z)); }
-
-// VEC consecutive elements of a row as floats (VEC * sizeof(E) = 16, or one element)
-template <typename E, int VEC> struct Raw;
-template <> struct Raw<__nv_bfloat16, 8> {
-  uint4 r;
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    r = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p) + i));
-  }
-  __device__ __forceinline__ void get(float* f) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-      w[k] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p) + i) =
-        make_uint4(w[0], w[1], w[2], w[3]);
-  }
-};
-template <> struct Raw<float, 4> {
-  float4 r;
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    r = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i));
-  }
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = r.x;
-    f[1] = r.y;
-    f[2] = r.z;
-    f[3] = r.w;
-  }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float* f) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) =
-        make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <typename E> struct Raw<E, 1> {
-  E r;
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    r = __ldg(reinterpret_cast<const E*>(p) + i);
-  }
-  __device__ __forceinline__ void get(float* f) const { f[0] = Elem<E>::to_f(r); }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float* f) {
-    reinterpret_cast<E*>(p)[i] = Elem<E>::from_f(f[0]);
-  }
-};
-
-// VEC fp32 weights from column `col` on (1 without weights); they stay in L1 between rows.
-template <int VEC>
-__device__ __forceinline__ void weights(const float* w, int col, float (&f)[VEC]) {
-  if (!w) {
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) f[k] = 1.f;
-  } else if constexpr (VEC == 1) {
-    f[0] = __ldg(w + col);
-  } else {
-#pragma unroll
-    for (int k = 0; k < VEC; k += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(w + col + k));
-      f[k] = v.x;
-      f[k + 1] = v.y;
-      f[k + 2] = v.z;
-      f[k + 3] = v.w;
-    }
-  }
-}
 
 // Sums of K values over the TPR threads of a row (every thread gets them).
 // Rows that span warps pass through shared memory; `buf` alternates between
@@ -140,45 +49,6 @@ __device__ __forceinline__ void row_sum(float (&v)[K], int tpr, float* buf, int&
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += b[(w0 + i) * K + k];
 }
-
-// First row of group g of a call with `groups` groups over T rows.
-__host__ __device__ __forceinline__ int64_t group_row(int64_t T, int groups, int g) {
-  return T * g / groups;
-}
-// The group that holds row t.
-__device__ __forceinline__ int row_group(int64_t T, int groups, int64_t t) {
-  int g = (int)(((t + 1) * groups - 1) / T);
-  while (g > 0 && group_row(T, groups, g) > t) --g;
-  while (g + 1 < groups && group_row(T, groups, g + 1) <= t) ++g;
-  return g;
-}
-
-// Sample of row t: the largest b with offsets[b] <= t (B when behind the last, -1 before the first).
-__device__ __forceinline__ int sample_of(const int32_t* offsets, int B, int64_t t) {
-  int lo = -1, hi = B;          // offsets[lo] <= t < offsets[hi + 1]
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)__ldg(offsets + mid) <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
-// Walks a group's rows keeping the sample of the current row.
-struct SampleWalk {
-  int b;
-  int64_t next;                  // first row of the next sample
-  __device__ __forceinline__ void seek(const NormArgs& a, int64_t t) {
-    b = sample_of(a.offsets, a.B, t);
-    next = b >= a.B ? (int64_t)1 << 62 : (int64_t)__ldg(a.offsets + b + 1);
-  }
-  // returns true when the sample changed
-  __device__ __forceinline__ bool at(const NormArgs& a, int64_t t) {
-    if (t < next) return false;
-    seek(a, t);
-    return true;
-  }
-  __device__ __forceinline__ bool live(const NormArgs& a) const { return b >= 0 && b < a.B; }
-};
 
 template <typename E, int VEC, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const NormArgs a, int tpr) {
@@ -543,9 +413,16 @@ constexpr int kMaxWidth = 8192;
 // How a call is cut: TPR threads to a row, rpb rows to a block, `groups` row ranges.
 struct Plan {
   int vec, nv, tpr, threads, rpb, groups, blocks;
+  StreamPlan stream;
 };
-Plan plan(int64_t T, int d, int dtype, bool backward) {
-  Plan p;
+Plan plan(int64_t T, int d, int dtype, bool backward, int gate_kind) {
+  Plan p = {};
+  p.stream = stream_plan(T, d, dtype, backward, gate_kind);
+  if (p.stream.nv) {
+    p.groups = p.stream.groups;
+    p.blocks = p.stream.blocks;
+    return p;
+  }
   const int v16 = dtype == GDPA_DTYPE_BF16 ? 8 : 4;
   p.vec = d % v16 == 0 ? v16 : 1;
   const int nvec = d / p.vec;
@@ -668,9 +545,10 @@ extern "C" gdpa_status_t gdpa_block_norm_fwd(const gdpa_block_norm_t* p, const i
   a.offsets = offsets;
   a.y = y;
   a.n = n;
-  const Plan pl = plan(p->T, p->d, p->dtype, false);
+  const Plan pl = plan(p->T, p->d, p->dtype, false, p->gate);
   a.groups = pl.groups;
   const cudaStream_t st = (cudaStream_t)stream;
+  if (pl.stream.nv) return finish(launch_norm_stream(a, pl.stream, p->dtype, false, st));
   return finish(p->dtype == GDPA_DTYPE_BF16 ? dispatch<__nv_bfloat16, 8>(a, pl, false, st)
                                             : dispatch<float, 4>(a, pl, false, st));
 }
@@ -680,7 +558,7 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd_workspace_size(const gdpa_block_nor
   const gdpa_status_t s = check_norm(p);
   if (s != GDPA_OK) return s;
   if (!bytes) return GDPA_ERR_INVALID_ARG;
-  *bytes = ws_bytes(plan(p->T, p->d, p->dtype, true), p->d, p->gate);
+  *bytes = ws_bytes(plan(p->T, p->d, p->dtype, true, p->gate), p->d, p->gate);
   return GDPA_OK;
 }
 
@@ -708,7 +586,7 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const i
   if (off16(y) || off16(f) || off16(gate) || off16(dy) || off16(dn) || off16(dx) || off16(df) ||
       off16(dgate) || off16(w_post) || off16(w_pre) || off4(dw_post) || off4(dw_pre) || off4(offsets))
     return GDPA_ERR_INVALID_ARG;
-  const Plan pl = plan(p->T, p->d, p->dtype, true);
+  const Plan pl = plan(p->T, p->d, p->dtype, true, p->gate);
   if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < ws_bytes(pl, p->d, p->gate))
     return GDPA_ERR_WORKSPACE;
   const cudaStream_t st = (cudaStream_t)stream;
@@ -740,8 +618,9 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const i
   a.part_post = w_post ? (float*)workspace : nullptr;
   a.part_pre = w_pre ? (float*)((char*)workspace + wpart) : nullptr;
   a.part_gate = (float*)((char*)workspace + 2 * wpart);
-  cudaError_t e = p->dtype == GDPA_DTYPE_BF16 ? dispatch<__nv_bfloat16, 8>(a, pl, true, st)
-                                              : dispatch<float, 4>(a, pl, true, st);
+  cudaError_t e = pl.stream.nv ? launch_norm_stream(a, pl.stream, p->dtype, true, st)
+                  : p->dtype == GDPA_DTYPE_BF16 ? dispatch<__nv_bfloat16, 8>(a, pl, true, st)
+                                                : dispatch<float, 4>(a, pl, true, st);
   if (e == cudaSuccess && (w_post || w_pre || p->gate == GDPA_GATE_SAMPLE)) {
     KernelScope ks_("gdpa_block_norm_join", st);
     const int cols = (p->d + 31) / 32;

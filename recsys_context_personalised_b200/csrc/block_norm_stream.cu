@@ -1,0 +1,582 @@
+// The block norm on rows streamed through shared memory (formulas: block_norm.cu).
+//
+// Bound: memory, every row once.  A row belongs to one warp (or to 2, 4 or 8 where it is
+// wide), a group of warps walks a contiguous range of rows, and every warp keeps the next rows of its
+// columns in flight by bulk copies into a ring of its own: the copies need no registers, so the
+// bytes in flight (100 to 190 KB an SM) do not depend on what the arithmetic holds, and a row's
+// reductions are shuffles within a warp that no other row waits for.  Measured at 132 k
+// rows of 2048 bf16 with a gate per element: see launch_norm_stream.
+//
+// The weights' gradients (and a shared gate's) accumulate in fp32 registers over the range, in the
+// rows' order, and go to the workspace once.
+#include <math.h>
+
+#include "block_norm.cuh"
+#include "sm100.cuh"
+
+namespace gdpa {
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarpsS = 16, kThreadsS = kWarpsS * 32;
+constexpr int kMaxFwd = 4, kMaxBwd = 2;              // 16-byte vectors of a row that a thread holds
+constexpr uint64_t kNormTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy wait is microseconds
+constexpr int kMaxStages = 8;
+constexpr uint32_t kRingBytes = 200 * 1024;          // of a block
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// 16 bytes of shared memory as pairs of floats (the arithmetic is in packed pairs: half the instructions)
+template <typename E>
+__device__ __forceinline__ void lds(uint32_t addr, float2* f) {
+  uint32_t w[4];
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr));
+  if constexpr (sizeof(E) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+  }
+}
+template <int P>
+__device__ __forceinline__ void weights2(const float* w, int col, float2 (&f)[P]) {
+#pragma unroll
+  for (int k = 0; k < P; k += 2) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(w + col + 2 * k));
+    f[k] = make_float2(v.x, v.y);
+    f[k + 1] = make_float2(v.z, v.w);
+  }
+}
+template <typename E, int P>
+__device__ __forceinline__ void put(void* p, int64_t i, const float2 (&f)[P]) {
+  Raw<E, 2 * P>::store(p, i, reinterpret_cast<const float*>(f));
+}
+template <typename E, int P>
+__device__ __forceinline__ void get(const void* p, int64_t i, float2 (&f)[P]) {
+  Raw<E, 2 * P> r;
+  r.load(p, i);
+  r.get(reinterpret_cast<float*>(f));
+}
+// act of the gate, by selection
+template <int P>
+__device__ __forceinline__ void act(float2 (&z)[P], int sigmoid) {
+#pragma unroll
+  for (int k = 0; k < P; ++k)
+    z[k] = make_float2(sigmoid ? logistic(z[k].x) : z[k].x, sigmoid ? logistic(z[k].y) : z[k].y);
+}
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+
+// The rows of one warp: its columns [col0, col0 + n) of the group's rows [t0, t1), NT tensors, in a
+// ring of `stages` rows.
+template <typename E, int NV, int NT>
+struct Stream {
+  static constexpr int VEC = 16 / sizeof(E), SEG = NV * 32 * VEC;
+  static constexpr uint32_t SEGB = SEG * sizeof(E), ROWB = NT * SEGB;
+  const E* src[NT];
+  uint32_t ring, bar;
+  int64_t t0, t1;
+  int d, n, stages, stage;
+  uint32_t phase;
+  volatile int* abort_flag;
+
+  __device__ __forceinline__ void issue(int64_t t, int slot, int lane) {
+    if (t < t1 && lane == 0) {
+      const uint32_t bytes = (uint32_t)n * sizeof(E);
+      mbar_expect_tx(bar + 8 * slot, bytes * NT);
+      if (n > 0)
+#pragma unroll
+        for (int k = 0; k < NT; ++k)
+          bulk_load(ring + slot * ROWB + k * SEGB, src[k] + t * d, bytes, bar + 8 * slot);
+    }
+  }
+  __device__ __forceinline__ void start(int lane) {
+    stage = 0;
+    phase = 0;
+    for (int s = 0; s < stages; ++s) issue(t0 + s, s, lane);
+  }
+  // Waits for the current row; false (its values are garbage) when the wait ran out.
+  __device__ __forceinline__ bool wait() {
+    const bool ok = mbar_wait(bar + 8 * stage, phase, abort_flag, kNormTimeoutNs);
+    return __all_sync(0xffffffffu, ok);
+  }
+  __device__ __forceinline__ uint32_t at(int k) const { return ring + stage * ROWB + k * SEGB; }
+  // The current row (t) has been read: its place takes a later one.
+  __device__ __forceinline__ void next(int64_t t, int lane) {
+    __syncwarp();
+    issue(t + stages, stage, lane);
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Sums of K values over a row's warps (every thread gets them): shuffles, then for a row of several
+// warps a pass through shared memory between them (two halves in turn, so one barrier is enough).
+template <int K>
+__device__ __forceinline__ void row_sum_w(float (&v)[K], int W, int wi, int gi, float* buf, int& flip) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (W == 1) return;
+  float* b = buf + flip * (kWarpsS * 3) + gi * W * K;
+  flip ^= 1;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) b[wi * K + k] = v[k];
+  named_bar_sync(1 + gi, W * 32);
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = 0.f;
+  for (int i = 0; i < W; ++i)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += b[i * K + k];
+}
+
+// What a call has is fixed at compile time (GATE: a gdpa_gate_t): branches on it inside the row would
+// make the compiler move the row's registers around.
+template <typename E, int NV, bool BLOCK, bool POST, int GATE>
+__global__ void __launch_bounds__(kThreadsS, 1)
+norm_stream_fwd_kernel(const NormArgs a, int W, int stages) {
+  using St = Stream<E, NV, BLOCK ? (GATE == GDPA_GATE_TOKEN ? 3 : 2) : 1>;
+  constexpr int VEC = St::VEC, P = VEC / 2;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarpsS * kMaxStages];
+  __shared__ float buf[2 * 3 * kWarpsS];
+  __shared__ int abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (kWarpsS / W) + gi;
+  if (threadIdx.x < kWarpsS * kMaxStages) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
+  if (threadIdx.x == 0) abort_s = 0;
+  fence_mbar_init();
+  __syncthreads();
+  St st;
+  const int col0 = wi * St::SEG;
+  st.n = max(0, min(St::SEG, a.d - col0));
+  st.d = a.d;
+  st.stages = stages;
+  st.src[0] = reinterpret_cast<const E*>(a.x) + col0;
+  if constexpr (BLOCK) st.src[1] = reinterpret_cast<const E*>(a.f) + col0;
+  if constexpr (GATE == GDPA_GATE_TOKEN) st.src[2] = reinterpret_cast<const E*>(a.gate) + col0;
+  st.ring = smem_u32(smem) + warp * (stages * St::ROWB);
+  st.bar = smem_u32(&bars[warp * kMaxStages]);
+  st.abort_flag = &abort_s;
+  st.t0 = g < a.groups ? group_row(a.T, a.groups, g) : 0;
+  st.t1 = g < a.groups ? group_row(a.T, a.groups, g + 1) : 0;
+  st.start(lane);
+  int flip = 0;
+  SampleWalk walk;
+  walk.next = -1;
+  walk.b = 0;
+  for (int64_t t = st.t0; t < st.t1; ++t) {
+    const float poison = st.wait() ? 1.f : NAN;
+    float2 y[NV][P];
+    bool live = true;
+    if constexpr (BLOCK) {
+      float scale = a.alpha * poison;
+      if constexpr (POST) {
+        float2 q[2] = {two(0.f), two(0.f)};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * 32 + lane) * VEC;
+          if (c < st.n) {
+            float2 f[P];
+            lds<E>(st.at(1) + c * sizeof(E), f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) q[k & 1] = __ffma2_rn(f[k], f[k], q[k & 1]);
+          }
+        }
+        float v[1] = {(q[0].x + q[1].x) + (q[0].y + q[1].y)};
+        row_sum_w(v, W, wi, gi, buf, flip);
+        scale *= 1.f / sqrtf(fmaf(v[0], a.inv_d, a.eps));
+      }
+      if constexpr (GATE == GDPA_GATE_SAMPLE) {
+        walk.at(a, t);
+        live = walk.live(a);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 + lane) * VEC;
+        if (c < st.n) {
+          float2 f[P], w[P];
+          lds<E>(st.at(0) + c * sizeof(E), y[i]);
+          lds<E>(st.at(1) + c * sizeof(E), f);
+#pragma unroll
+          for (int k = 0; k < P; ++k) f[k] = __fmul2_rn(f[k], two(scale));
+          if constexpr (POST) {
+            weights2<P>(a.w_post, col0 + c, w);
+#pragma unroll
+            for (int k = 0; k < P; ++k) f[k] = __fmul2_rn(f[k], w[k]);
+          }
+          if constexpr (GATE != GDPA_GATE_NONE) {
+            if constexpr (GATE == GDPA_GATE_TOKEN)
+              lds<E>(st.at(2) + c * sizeof(E), w);
+            else
+              get<E>(a.gate, (int64_t)(live ? walk.b : 0) * a.d + col0 + c, w);
+            act(w, a.sigmoid);
+          }
+#pragma unroll
+          for (int k = 0; k < P; ++k)
+            y[i][k] = GATE != GDPA_GATE_NONE ? __ffma2_rn(w[k], f[k], y[i][k]) : __fadd2_rn(f[k], y[i][k]);
+          if (live) put<E>(a.y, t * a.d + col0 + c, y[i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 + lane) * VEC;
+        if (c < st.n) {
+          lds<E>(st.at(0) + c * sizeof(E), y[i]);
+#pragma unroll
+          for (int k = 0; k < P; ++k) y[i][k] = __fmul2_rn(y[i][k], two(poison));
+        }
+      }
+    }
+    st.next(t, lane);
+    if (a.w_pre) {
+      float2 q[2] = {two(0.f), two(0.f)};
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if ((i * 32 + lane) * VEC < st.n)
+#pragma unroll
+          for (int k = 0; k < P; ++k) q[k & 1] = __ffma2_rn(y[i][k], y[i][k], q[k & 1]);
+      float v[1] = {(q[0].x + q[1].x) + (q[0].y + q[1].y)};
+      row_sum_w(v, W, wi, gi, buf, flip);
+      const float scale = 1.f / sqrtf(fmaf(v[0], a.inv_d, a.eps));
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 + lane) * VEC;
+        if (c < st.n && live) {
+          float2 w[P];
+          weights2<P>(a.w_pre, col0 + c, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) y[i][k] = __fmul2_rn(y[i][k], __fmul2_rn(w[k], two(scale)));
+          put<E>(a.n, t * a.d + col0 + c, y[i]);
+        }
+      }
+    }
+  }
+}
+
+// (A gate of GDPA_GATE_SAMPLE is one row per sample, whose gradient accumulates over the sample's rows.)
+template <typename E, int NV, bool BLOCK, bool PRE, bool POST, int GATE>
+__global__ void __launch_bounds__(kThreadsS, 1)
+norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
+  constexpr bool SHARED = GATE == GDPA_GATE_SAMPLE;
+  // the tensors, in the order dy, y, dn, f, token gate
+  constexpr int KY = 1, KN = 2, KF = PRE ? 3 : 1, KZ = KF + 1;
+  using St = Stream<E, NV, KF + (BLOCK ? 1 : 0) + (GATE == GDPA_GATE_TOKEN ? 1 : 0)>;
+  constexpr int VEC = St::VEC, P = VEC / 2;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t bars[kWarpsS * kMaxStages];
+  __shared__ float buf[2 * 3 * kWarpsS];
+  __shared__ int abort_s;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (kWarpsS / W) + gi;
+  if (threadIdx.x < kWarpsS * kMaxStages) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
+  if (threadIdx.x == 0) abort_s = 0;
+  fence_mbar_init();
+  __syncthreads();
+  St st;
+  const int col0 = wi * St::SEG;
+  st.n = max(0, min(St::SEG, a.d - col0));
+  st.d = a.d;
+  st.stages = stages;
+  st.src[0] = reinterpret_cast<const E*>(a.dy ? a.dy : a.dn) + col0;     // (no dy: unused)
+  if constexpr (PRE) {
+    st.src[KY] = reinterpret_cast<const E*>(a.x) + col0;
+    st.src[KN] = reinterpret_cast<const E*>(a.dn) + col0;
+  }
+  if constexpr (BLOCK) st.src[KF] = reinterpret_cast<const E*>(a.f) + col0;
+  if constexpr (GATE == GDPA_GATE_TOKEN) st.src[KZ] = reinterpret_cast<const E*>(a.gate) + col0;
+  st.ring = smem_u32(smem) + warp * (stages * St::ROWB);
+  st.bar = smem_u32(&bars[warp * kMaxStages]);
+  st.abort_flag = &abort_s;
+  st.t0 = g < a.groups ? group_row(a.T, a.groups, g) : 0;
+  st.t1 = g < a.groups ? group_row(a.T, a.groups, g + 1) : 0;
+  st.start(lane);
+  int flip = 0;
+  float2 apost[NV][P], apre[NV][P], agate[SHARED ? NV : 1][P];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      apost[i][k] = apre[i][k] = two(0.f);
+      if (SHARED) agate[i][k] = two(0.f);
+    }
+  SampleWalk walk;
+  walk.next = -1;
+  walk.b = 0;
+  // act(gate) of 8 or 4 columns: from the ring, or from the sample's row
+  auto gate_at = [&](int c, float2 (&z)[P]) {
+    if constexpr (SHARED)
+      get<E>(a.gate, (int64_t)walk.b * a.d + col0 + c, z);
+    else if constexpr (GATE == GDPA_GATE_TOKEN)
+      lds<E>(st.at(KZ) + c * sizeof(E), z);
+    act(z, a.sigmoid);
+  };
+  // act'(gate) from act(gate)
+  auto slope = [&](const float2 z) -> float2 {
+    const float2 v = __ffma2_rn(make_float2(-z.x, -z.y), z, z);
+    return make_float2(a.sigmoid ? v.x : 1.f, a.sigmoid ? v.y : 1.f);
+  };
+  // the rows of sample walk.b that this group holds are done: their gate gradient goes out whole, or as
+  // a piece (slot 1 when it holds the sample's first row)
+  auto flush = [&]() {
+    if (!SHARED || !walk.live(a)) return;
+    const int64_t lo = max((int64_t)__ldg(a.offsets + walk.b), (int64_t)0);
+    const int64_t hi = min(walk.next, a.T);
+    float* out = lo >= st.t0 && hi <= st.t1
+                     ? a.dgate_sample + (int64_t)walk.b * a.d
+                     : a.part_gate + ((int64_t)g * 2 + (lo >= st.t0 ? 1 : 0)) * a.d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 + lane) * VEC;
+      if (c < st.n) {
+        float2 z[P];
+        gate_at(c, z);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          float2& acc = agate[SHARED ? i : 0][k];
+          *reinterpret_cast<float2*>(out + col0 + c + 2 * k) = __fmul2_rn(acc, slope(z[k]));
+          acc = two(0.f);
+        }
+      }
+    }
+  };
+  for (int64_t t = st.t0; t < st.t1; ++t) {
+    const float poison = st.wait() ? 1.f : NAN;
+    bool live = true;
+    if (SHARED) {
+      if (t >= walk.next) {
+        if (t > st.t0) flush();
+        walk.seek(a, t);
+      }
+      live = walk.live(a);
+    }
+    if (!live) {                       // (the same for all of the row's warps) adds nothing anywhere
+      st.next(t, lane);
+      continue;
+    }
+    float2 q[3] = {two(0.f), two(0.f), two(0.f)};      // sums of y^2, w_pre dn y and f^2
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 + lane) * VEC;
+      if (c < st.n) {
+        if constexpr (PRE) {
+          float2 y[P], dn[P], w[P];
+          lds<E>(st.at(KY) + c * sizeof(E), y);
+          lds<E>(st.at(KN) + c * sizeof(E), dn);
+          weights2<P>(a.w_pre, col0 + c, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            q[0] = __ffma2_rn(y[k], y[k], q[0]);
+            q[1] = __ffma2_rn(__fmul2_rn(dn[k], w[k]), y[k], q[1]);
+          }
+        }
+        if constexpr (POST) {
+          float2 f[P];
+          lds<E>(st.at(KF) + c * sizeof(E), f);
+#pragma unroll
+          for (int k = 0; k < P; ++k) q[2] = __ffma2_rn(f[k], f[k], q[2]);
+        }
+      }
+    }
+    float v[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
+    if constexpr (PRE || POST) row_sum_w(v, W, wi, gi, buf, flip);
+    const float sy = poison / sqrtf(fmaf(v[0], a.inv_d, a.eps));
+    const float my = v[1] * sy * a.inv_d;                  // mean(w_pre dn yh)
+    const float sf = POST ? 1.f / sqrtf(fmaf(v[2], a.inv_d, a.eps)) : 1.f;
+    float2 m2v = two(0.f);
+    float2 G[NV][P];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 + lane) * VEC;
+      if (c < st.n) {
+        lds<E>(st.at(0) + c * sizeof(E), G[i]);
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+          G[i][k] = make_float2(a.dy ? G[i][k].x : 0.f, a.dy ? G[i][k].y : 0.f);
+        if constexpr (PRE) {
+          float2 y[P], dn[P], w[P];
+          lds<E>(st.at(KY) + c * sizeof(E), y);
+          lds<E>(st.at(KN) + c * sizeof(E), dn);
+          weights2<P>(a.w_pre, col0 + c, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const float2 yh = __fmul2_rn(y[k], two(sy));
+            G[i][k] = __ffma2_rn(two(sy), __ffma2_rn(yh, two(-my), __fmul2_rn(dn[k], w[k])), G[i][k]);
+            apre[i][k] = __ffma2_rn(dn[k], yh, apre[i][k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(poison));
+        }
+        put<E>(a.dx, t * a.d + col0 + c, G[i]);
+        if constexpr (POST) {
+          float2 f[P], z[P], w[P];
+          lds<E>(st.at(KF) + c * sizeof(E), f);
+          if constexpr (GATE != GDPA_GATE_NONE) gate_at(c, z);
+          weights2<P>(a.w_post, col0 + c, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const float2 fh = __fmul2_rn(f[k], two(sf));
+            float2 du = __fmul2_rn(two(a.alpha), G[i][k]);
+            if constexpr (GATE != GDPA_GATE_NONE) du = __fmul2_rn(z[k], du);
+            const float2 e = __fmul2_rn(du, fh);
+            apost[i][k] = __fadd2_rn(apost[i][k], e);
+            m2v = __ffma2_rn(e, w[k], m2v);
+          }
+        }
+      }
+    }
+    float m2[1] = {m2v.x + m2v.y};
+    if constexpr (POST) row_sum_w(m2, W, wi, gi, buf, flip);
+    const float mf = m2[0] * a.inv_d;
+    if constexpr (BLOCK) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 + lane) * VEC;
+        if (c < st.n) {
+          float2 f[P], z[P], w[P];
+          lds<E>(st.at(KF) + c * sizeof(E), f);
+          if constexpr (POST) weights2<P>(a.w_post, col0 + c, w);
+          if constexpr (GATE != GDPA_GATE_NONE) gate_at(c, z);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const float2 fh = POST ? __fmul2_rn(f[k], two(sf)) : f[k];
+            const float2 gw = __fmul2_rn(POST ? __fmul2_rn(G[i][k], w[k]) : G[i][k], two(a.alpha));
+            float2 wd = gw;
+            if constexpr (GATE != GDPA_GATE_NONE) {
+              const float2 gu = __fmul2_rn(gw, fh);                     // alpha G u
+              wd = __fmul2_rn(gw, z[k]);
+              if constexpr (SHARED)
+                agate[i][k] = __fadd2_rn(agate[i][k], gu);
+              else
+                z[k] = __fmul2_rn(gu, slope(z[k]));
+            }
+            f[k] = POST ? __fmul2_rn(two(sf), __ffma2_rn(fh, two(-mf), wd)) : wd;
+          }
+          put<E>(a.df, t * a.d + col0 + c, f);
+          if constexpr (GATE == GDPA_GATE_TOKEN) put<E>(a.dgate, t * a.d + col0 + c, z);
+        }
+      }
+    }
+    st.next(t, lane);
+  }
+  if (SHARED && st.t1 > st.t0) flush();
+  // the block's weight gradients: its groups in order, through shared memory (every copy has been read)
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem);
+  for (int which = 0; which < 2; ++which) {
+    float* out = which ? a.part_pre : a.part_post;
+    if (!out) continue;
+    for (int r = 0; r < kWarpsS / W; ++r) {
+      if (gi == r)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = (i * 32 + lane) * VEC;
+          if (c < st.n)
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              const float2 v = which ? apre[i][k] : apost[i][k];
+              float2* at = reinterpret_cast<float2*>(sums + col0 + c) + k;
+              *at = r == 0 ? v : __fadd2_rn(*at, v);
+            }
+        }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.d; c += kThreadsS) out[(int64_t)blockIdx.x * a.d + c] = sums[c];
+    __syncthreads();
+  }
+}
+
+using Kernel = void (*)(const NormArgs, int, int);
+
+template <typename E, int NV, bool BACKWARD, bool PRE, bool POST, int GATE>
+Kernel kernel_of() {
+  if constexpr (BACKWARD)
+    return norm_stream_bwd_kernel<E, NV, true, PRE, POST, GATE>;
+  else
+    return norm_stream_fwd_kernel<E, NV, true, POST, GATE>;
+}
+template <typename E, int NV, bool BACKWARD, bool PRE, bool POST>
+Kernel kernel_of(const NormArgs& a) {
+  if (a.gate_kind == GDPA_GATE_TOKEN) return kernel_of<E, NV, BACKWARD, PRE, POST, GDPA_GATE_TOKEN>();
+  if (a.gate_kind == GDPA_GATE_SAMPLE) return kernel_of<E, NV, BACKWARD, PRE, POST, GDPA_GATE_SAMPLE>();
+  return kernel_of<E, NV, BACKWARD, PRE, POST, GDPA_GATE_NONE>();
+}
+template <typename E, int NV, bool BACKWARD>
+Kernel kernel_of(const NormArgs& a) {
+  if (!a.f) {
+    if constexpr (BACKWARD)
+      return norm_stream_bwd_kernel<E, NV, false, true, false, GDPA_GATE_NONE>;
+    else
+      return norm_stream_fwd_kernel<E, NV, false, false, GDPA_GATE_NONE>;
+  }
+  if constexpr (BACKWARD)             // (forward, n is a test beside the row's sum)
+    if (!a.w_pre)
+      return a.w_post ? kernel_of<E, NV, BACKWARD, false, true>(a) : kernel_of<E, NV, BACKWARD, false, false>(a);
+  return a.w_post ? kernel_of<E, NV, BACKWARD, true, true>(a) : kernel_of<E, NV, BACKWARD, true, false>(a);
+}
+
+template <typename E>
+Kernel dispatch(const NormArgs& a, int nv, bool backward) {
+  if (backward) return nv == kMaxBwd ? kernel_of<E, kMaxBwd, true>(a) : kernel_of<E, kMaxBwd / 2, true>(a);
+  return nv == kMaxFwd ? kernel_of<E, kMaxFwd, false>(a) : kernel_of<E, kMaxFwd / 2, false>(a);
+}
+
+}  // namespace
+
+StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind) {
+  StreamPlan p = {};
+  const int tensors = (backward ? 4 : 2) + (gate_kind == GDPA_GATE_TOKEN ? 1 : 0);   // at most
+  const int es = dtype == GDPA_DTYPE_BF16 ? 2 : 4, vec = 16 / es;
+  // rows of whole 16-byte units, at least a warp's width
+  if (d % vec || d < 32 * vec) return p;
+  const int most = backward ? kMaxBwd : kMaxFwd;
+  int nv = most / 2;
+  while (nv < most && nv * 32 * vec < d) nv *= 2;
+  int w = 1;
+  while (w * nv * 32 * vec < d) w *= 2;
+  if (w > kWarpsS) return p;
+  const int64_t groups = (int64_t)device_sm_count() * (kWarpsS / w);
+  // a range of a few rows at least: below that the registers' form has its first rows sooner
+  if (T < 4 * groups) return p;
+  const uint32_t row = (uint32_t)(nv * 32 * vec * es) * tensors;
+  int stages = (int)(kRingBytes / kWarpsS / row);
+  if (stages < 2) return p;
+  p.nv = nv;
+  p.warps_row = w;
+  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  p.groups = (int)groups;
+  p.blocks = device_sm_count();
+  p.smem = (size_t)p.stages * row * kWarpsS;
+  if (backward && p.smem < (size_t)d * 4) p.smem = (size_t)d * 4;
+  return p;
+}
+
+cudaError_t launch_norm_stream(const NormArgs& a, const StreamPlan& p, int dtype, bool backward,
+                               cudaStream_t st) {
+  Kernel kern = dtype == GDPA_DTYPE_BF16 ? dispatch<__nv_bfloat16>(a, p.nv, backward)
+                                         : dispatch<float>(a, p.nv, backward);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  if (e != cudaSuccess) return e;
+  KernelScope ks_(backward ? "gdpa_block_norm_bwd" : "gdpa_block_norm_fwd", st);
+  kern<<<p.blocks, kThreadsS, p.smem, st>>>(a, p.warps_row, p.stages);
+  return cudaGetLastError();
+}
+
+}  // namespace gdpa

@@ -475,6 +475,18 @@ def test_norm_shared_gates(n, d):
     _check_norm(n, d, torch.bfloat16, "sample", seed=len(n) + d, pad=6)
 
 
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 256), (torch.bfloat16, 776), (torch.bfloat16, 1024),
+                                     (torch.bfloat16, 2056), (torch.bfloat16, 5000), (torch.bfloat16, 8192),
+                                     (torch.float32, 128), (torch.float32, 1000), (torch.float32, 1540),
+                                     (torch.float32, 4096)])
+@pytest.mark.parametrize("gate,post,pre", [("token", True, True), ("sample", True, True), (None, False, True),
+                                           ("sample", False, False), (None, True, False)])
+def test_norm_streamed_rows(dtype, d, gate, post, pre):
+    """Enough rows for every group of warps to walk a range: rows of one to eight warps, whole and cut last
+    segments, samples that span several groups, rows behind the last sample."""
+    _check_norm([2000, 0, 1, 2900], d, dtype, gate, post, pre, seed=d, pad=7 if gate == "sample" else 0)
+
+
 @pytest.mark.parametrize("std", [0.0, 1e-6, 1e6])
 def test_norm_scales(std):
     """Rows of zeros (the root holds eps alone), tiny and huge rows."""
