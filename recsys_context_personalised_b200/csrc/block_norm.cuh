@@ -145,7 +145,7 @@ struct SampleWalk {
 
 // How a call of the streaming kernels is cut (nv = 0: they do not take it).
 struct StreamPlan {
-  int nv, warps_row, stages, groups, blocks;
+  int nv, warps_row, warps, groups, blocks;
   size_t smem;
 };
 StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind);

@@ -3,9 +3,10 @@
 // Bound: memory, every row once.  A row belongs to one warp (or to 2, 4 or 8 where it is
 // wide), a group of warps walks a contiguous range of rows, and every warp keeps the next rows of its
 // columns in flight by bulk copies into a ring of its own: the copies need no registers, so the
-// bytes in flight (100 to 190 KB an SM) do not depend on what the arithmetic holds, and a row's
-// reductions are shuffles within a warp that no other row waits for.  Measured at 132 k
-// rows of 2048 bf16 with a gate per element: see launch_norm_stream.
+// bytes in flight (about 100 KB an SM) do not depend on what the arithmetic holds, and a row's
+// reductions are shuffles within a warp, or a barrier of a row's few warps, that no other row waits for.
+// Measured (copy: 6.5 TB/s): 132 k rows of 2048 bf16 with a gate per element forward 447 us, 6.1 TB/s; 126 k rows
+// of 1024 backward, with a gate per element 360 us, 5.7 TB/s, with shared gates 330 us, 4.7 TB/s.
 //
 // The weights' gradients (and a shared gate's) accumulate in fp32 registers over the range, in the
 // rows' order, and go to the workspace once.
@@ -19,11 +20,16 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarpsS = 16, kThreadsS = kWarpsS * 32;
-constexpr int kMaxFwd = 4, kMaxBwd = 2;              // 16-byte vectors of a row that a thread holds
+// Warps of a block (one block to an SM) and 16-byte vectors of a row that a thread holds: forward y in
+// fp32 (4 vectors: 467 us at 2048 wide instead of 447, 8 in 8 warps: 635); backward y, dn, f, G, the gate and up
+// to three sums, for which 16 warps have too few registers and 8 hide too little (1024 wide, shared
+// gates: 496 and 458 us where 12 warps took 360).
+constexpr int kWarpsFwd = 16, kWarpsBwd = 12, kMaxFwd = 2, kMaxBwd = 2;
 constexpr uint64_t kNormTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy wait is microseconds
-constexpr int kMaxStages = 8;
-constexpr uint32_t kRingBytes = 200 * 1024;          // of a block
+// Rows in flight of a warp, the current one among them.  Two are enough, and what a longer ring takes is missing
+// in L1, which holds the weights: backward, 1024 wide, 4 rows 360 us, 2 rows 326 us.
+constexpr int kStages = 2;
+constexpr uint32_t kRingBytes = 200 * 1024;          // of a block, at most; up to 24 KB of sums come behind it
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -78,7 +84,7 @@ __device__ __forceinline__ void act(float2 (&z)[P], int sigmoid) {
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 
 // The rows of one warp: its columns [col0, col0 + n) of the group's rows [t0, t1), NT tensors, in a
-// ring of `stages` rows.
+// ring of kStages rows.
 template <typename E, int NV, int NT>
 struct Stream {
   static constexpr int VEC = 16 / sizeof(E), SEG = NV * 32 * VEC;
@@ -86,7 +92,7 @@ struct Stream {
   const E* src[NT];
   uint32_t ring, bar;
   int64_t t0, t1;
-  int d, n, stages, stage;
+  int d, n, stage;
   uint32_t phase;
   volatile int* abort_flag;
 
@@ -103,7 +109,7 @@ struct Stream {
   __device__ __forceinline__ void start(int lane) {
     stage = 0;
     phase = 0;
-    for (int s = 0; s < stages; ++s) issue(t0 + s, s, lane);
+    for (int s = 0; s < kStages; ++s) issue(t0 + s, s, lane);
   }
   // Waits for the current row; false (its values are garbage) when the wait ran out.
   __device__ __forceinline__ bool wait() {
@@ -114,8 +120,8 @@ struct Stream {
   // The current row (t) has been read: its place takes a later one.
   __device__ __forceinline__ void next(int64_t t, int lane) {
     __syncwarp();
-    issue(t + stages, stage, lane);
-    if (++stage == stages) {
+    issue(t + kStages, stage, lane);
+    if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
     }
@@ -131,7 +137,7 @@ __device__ __forceinline__ void row_sum_w(float (&v)[K], int W, int wi, int gi, 
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if (W == 1) return;
-  float* b = buf + flip * (kWarpsS * 3) + gi * W * K;
+  float* b = buf + flip * (kWarpsFwd * 3) + gi * W * K;
   flip ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -147,17 +153,17 @@ __device__ __forceinline__ void row_sum_w(float (&v)[K], int W, int wi, int gi, 
 // What a call has is fixed at compile time (GATE: a gdpa_gate_t): branches on it inside the row would
 // make the compiler move the row's registers around.
 template <typename E, int NV, bool BLOCK, bool POST, int GATE>
-__global__ void __launch_bounds__(kThreadsS, 1)
-norm_stream_fwd_kernel(const NormArgs a, int W, int stages) {
+__global__ void __launch_bounds__(kWarpsFwd * 32, 1)
+norm_stream_fwd_kernel(const NormArgs a, int W) {
   using St = Stream<E, NV, BLOCK ? (GATE == GDPA_GATE_TOKEN ? 3 : 2) : 1>;
   constexpr int VEC = St::VEC, P = VEC / 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[kWarpsS * kMaxStages];
-  __shared__ float buf[2 * 3 * kWarpsS];
+  __shared__ __align__(8) uint64_t bars[kWarpsFwd * kStages];
+  __shared__ float buf[2 * 3 * kWarpsFwd];
   __shared__ int abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (kWarpsS / W) + gi;
-  if (threadIdx.x < kWarpsS * kMaxStages) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
+  const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (blockDim.x / 32 / W) + gi;
+  if (threadIdx.x < kWarpsFwd * kStages) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
   if (threadIdx.x == 0) abort_s = 0;
   fence_mbar_init();
   __syncthreads();
@@ -165,12 +171,11 @@ norm_stream_fwd_kernel(const NormArgs a, int W, int stages) {
   const int col0 = wi * St::SEG;
   st.n = max(0, min(St::SEG, a.d - col0));
   st.d = a.d;
-  st.stages = stages;
   st.src[0] = reinterpret_cast<const E*>(a.x) + col0;
   if constexpr (BLOCK) st.src[1] = reinterpret_cast<const E*>(a.f) + col0;
   if constexpr (GATE == GDPA_GATE_TOKEN) st.src[2] = reinterpret_cast<const E*>(a.gate) + col0;
-  st.ring = smem_u32(smem) + warp * (stages * St::ROWB);
-  st.bar = smem_u32(&bars[warp * kMaxStages]);
+  st.ring = smem_u32(smem) + warp * (kStages * St::ROWB);
+  st.bar = smem_u32(&bars[warp * kStages]);
   st.abort_flag = &abort_s;
   st.t0 = g < a.groups ? group_row(a.T, a.groups, g) : 0;
   st.t1 = g < a.groups ? group_row(a.T, a.groups, g + 1) : 0;
@@ -199,7 +204,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W, int stages) {
         }
         float v[1] = {(q[0].x + q[1].x) + (q[0].y + q[1].y)};
         row_sum_w(v, W, wi, gi, buf, flip);
-        scale *= 1.f / sqrtf(fmaf(v[0], a.inv_d, a.eps));
+        scale *= rsqrtf(fmaf(v[0], a.inv_d, a.eps));
       }
       if constexpr (GATE == GDPA_GATE_SAMPLE) {
         walk.at(a, t);
@@ -253,7 +258,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W, int stages) {
           for (int k = 0; k < P; ++k) q[k & 1] = __ffma2_rn(y[i][k], y[i][k], q[k & 1]);
       float v[1] = {(q[0].x + q[1].x) + (q[0].y + q[1].y)};
       row_sum_w(v, W, wi, gi, buf, flip);
-      const float scale = 1.f / sqrtf(fmaf(v[0], a.inv_d, a.eps));
+      const float scale = rsqrtf(fmaf(v[0], a.inv_d, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * 32 + lane) * VEC;
@@ -271,20 +276,20 @@ norm_stream_fwd_kernel(const NormArgs a, int W, int stages) {
 
 // (A gate of GDPA_GATE_SAMPLE is one row per sample, whose gradient accumulates over the sample's rows.)
 template <typename E, int NV, bool BLOCK, bool PRE, bool POST, int GATE>
-__global__ void __launch_bounds__(kThreadsS, 1)
-norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
+__global__ void __launch_bounds__(kWarpsBwd * 32, 1)
+norm_stream_bwd_kernel(const NormArgs a, int W) {
   constexpr bool SHARED = GATE == GDPA_GATE_SAMPLE;
   // the tensors, in the order dy, y, dn, f, token gate
   constexpr int KY = 1, KN = 2, KF = PRE ? 3 : 1, KZ = KF + 1;
   using St = Stream<E, NV, KF + (BLOCK ? 1 : 0) + (GATE == GDPA_GATE_TOKEN ? 1 : 0)>;
   constexpr int VEC = St::VEC, P = VEC / 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t bars[kWarpsS * kMaxStages];
-  __shared__ float buf[2 * 3 * kWarpsS];
+  __shared__ __align__(8) uint64_t bars[kWarpsFwd * kStages];
+  __shared__ float buf[2 * 3 * kWarpsFwd];
   __shared__ int abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (kWarpsS / W) + gi;
-  if (threadIdx.x < kWarpsS * kMaxStages) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
+  const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (blockDim.x / 32 / W) + gi;
+  if (threadIdx.x < kWarpsFwd * kStages) mbar_init(smem_u32(&bars[threadIdx.x]), 1);
   if (threadIdx.x == 0) abort_s = 0;
   fence_mbar_init();
   __syncthreads();
@@ -292,7 +297,6 @@ norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
   const int col0 = wi * St::SEG;
   st.n = max(0, min(St::SEG, a.d - col0));
   st.d = a.d;
-  st.stages = stages;
   st.src[0] = reinterpret_cast<const E*>(a.dy ? a.dy : a.dn) + col0;     // (no dy: unused)
   if constexpr (PRE) {
     st.src[KY] = reinterpret_cast<const E*>(a.x) + col0;
@@ -300,68 +304,102 @@ norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
   }
   if constexpr (BLOCK) st.src[KF] = reinterpret_cast<const E*>(a.f) + col0;
   if constexpr (GATE == GDPA_GATE_TOKEN) st.src[KZ] = reinterpret_cast<const E*>(a.gate) + col0;
-  st.ring = smem_u32(smem) + warp * (stages * St::ROWB);
-  st.bar = smem_u32(&bars[warp * kMaxStages]);
+  st.ring = smem_u32(smem) + warp * (kStages * St::ROWB);
+  st.bar = smem_u32(&bars[warp * kStages]);
   st.abort_flag = &abort_s;
   st.t0 = g < a.groups ? group_row(a.T, a.groups, g) : 0;
   st.t1 = g < a.groups ? group_row(a.T, a.groups, g + 1) : 0;
   st.start(lane);
   int flip = 0;
-  float2 apost[NV][P], apre[NV][P], agate[SHARED ? NV : 1][P];
+  float2 apost[SHARED ? 1 : NV][P], apre[NV][P], agate[SHARED ? NV : 1][P];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int k = 0; k < P; ++k) {
-      apost[i][k] = apre[i][k] = two(0.f);
-      if (SHARED) agate[i][k] = two(0.f);
+      apre[i][k] = two(0.f);
+      if constexpr (SHARED) agate[i][k] = two(0.f);
+      if constexpr (!SHARED) apost[i][k] = two(0.f);
     }
+  // A shared gate: agate holds the sum over the sample's rows of alpha G fh, of which both the gate's
+  // gradient (times w_post act') and w_post's (times act) are made when the sample ends; the latter's sum
+  // stays in shared memory between samples.
+  float2* const spost = reinterpret_cast<float2*>(smem + (size_t)(blockDim.x / 32) * kStages * St::ROWB +
+                                                  (size_t)warp * St::SEG * 4);
+  if constexpr (SHARED && POST)
+    for (int c = lane; c < St::SEG / 2; c += 32) spost[c] = two(0.f);
   SampleWalk walk;
   walk.next = -1;
   walk.b = 0;
-  // act(gate) of 8 or 4 columns: from the ring, or from the sample's row
-  auto gate_at = [&](int c, float2 (&z)[P]) {
-    if constexpr (SHARED)
-      get<E>(a.gate, (int64_t)walk.b * a.d + col0 + c, z);
-    else if constexpr (GATE == GDPA_GATE_TOKEN)
-      lds<E>(st.at(KZ) + c * sizeof(E), z);
-    act(z, a.sigmoid);
-  };
+  // act(gate) of this thread's columns: of this row, or of this sample (times w_post)
+  float2 z[GATE != GDPA_GATE_NONE ? NV : 1][P];
   // act'(gate) from act(gate)
-  auto slope = [&](const float2 z) -> float2 {
-    const float2 v = __ffma2_rn(make_float2(-z.x, -z.y), z, z);
+  auto slope = [&](const float2 s) -> float2 {
+    const float2 v = __ffma2_rn(make_float2(-s.x, -s.y), s, s);
     return make_float2(a.sigmoid ? v.x : 1.f, a.sigmoid ? v.y : 1.f);
   };
   // the rows of sample walk.b that this group holds are done: their gate gradient goes out whole, or as
   // a piece (slot 1 when it holds the sample's first row)
   auto flush = [&]() {
-    if (!SHARED || !walk.live(a)) return;
-    const int64_t lo = max((int64_t)__ldg(a.offsets + walk.b), (int64_t)0);
-    const int64_t hi = min(walk.next, a.T);
-    float* out = lo >= st.t0 && hi <= st.t1
-                     ? a.dgate_sample + (int64_t)walk.b * a.d
-                     : a.part_gate + ((int64_t)g * 2 + (lo >= st.t0 ? 1 : 0)) * a.d;
+    if constexpr (SHARED) {
+      if (!walk.live(a)) return;
+      const int64_t lo = max((int64_t)__ldg(a.offsets + walk.b), (int64_t)0);
+      const int64_t hi = min(walk.next, a.T);
+      float* out = lo >= st.t0 && hi <= st.t1
+                       ? a.dgate_sample + (int64_t)walk.b * a.d
+                       : a.part_gate + ((int64_t)g * 2 + (lo >= st.t0 ? 1 : 0)) * a.d;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * 32 + lane) * VEC;
-      if (c < st.n) {
-        float2 z[P];
-        gate_at(c, z);
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 + lane) * VEC;
+        if (c < st.n) {
+          float2 s[P], w[P];
+          get<E>(a.gate, (int64_t)walk.b * a.d + col0 + c, s);
+          act(s, a.sigmoid);
+          if constexpr (POST) weights2<P>(a.w_post, col0 + c, w);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          float2& acc = agate[SHARED ? i : 0][k];
-          *reinterpret_cast<float2*>(out + col0 + c + 2 * k) = __fmul2_rn(acc, slope(z[k]));
-          acc = two(0.f);
+          for (int k = 0; k < P; ++k) {
+            const float2 sum = agate[i][k];
+            agate[i][k] = two(0.f);
+            *reinterpret_cast<float2*>(out + col0 + c + 2 * k) =
+                __fmul2_rn(POST ? __fmul2_rn(sum, w[k]) : sum, slope(s[k]));
+            if constexpr (POST) spost[c / 2 + k] = __ffma2_rn(sum, s[k], spost[c / 2 + k]);
+          }
         }
       }
     }
   };
+  // (columns past the row hold zeros throughout and are never stored)
+  float2 y[PRE ? NV : 1][P], dn[PRE ? NV : 1][P], f[BLOCK ? NV : 1][P], G[NV][P];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      G[i][k] = two(0.f);
+      if constexpr (PRE) y[i][k] = dn[i][k] = two(0.f);
+      if constexpr (BLOCK) f[i][k] = two(0.f);
+      if constexpr (GATE != GDPA_GATE_NONE) z[i][k] = two(0.f);
+    }
   for (int64_t t = st.t0; t < st.t1; ++t) {
     const float poison = st.wait() ? 1.f : NAN;
     bool live = true;
-    if (SHARED) {
+    if constexpr (SHARED) {
       if (t >= walk.next) {
         if (t > st.t0) flush();
         walk.seek(a, t);
+        if (walk.live(a))
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int c = (i * 32 + lane) * VEC;
+            if (c < st.n) {
+              get<E>(a.gate, (int64_t)walk.b * a.d + col0 + c, z[i]);
+              act(z[i], a.sigmoid);
+              if constexpr (POST) {
+                float2 w[P];
+                weights2<P>(a.w_post, col0 + c, w);
+#pragma unroll
+                for (int k = 0; k < P; ++k) z[i][k] = __fmul2_rn(z[i][k], w[k]);
+              }
+            }
+          }
       }
       live = walk.live(a);
     }
@@ -369,74 +407,83 @@ norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
       st.next(t, lane);
       continue;
     }
-    float2 q[3] = {two(0.f), two(0.f), two(0.f)};      // sums of y^2, w_pre dn y and f^2
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * 32 + lane) * VEC;
-      if (c < st.n) {
-        if constexpr (PRE) {
-          float2 y[P], dn[P], w[P];
-          lds<E>(st.at(KY) + c * sizeof(E), y);
-          lds<E>(st.at(KN) + c * sizeof(E), dn);
-          weights2<P>(a.w_pre, col0 + c, w);
-#pragma unroll
-          for (int k = 0; k < P; ++k) {
-            q[0] = __ffma2_rn(y[k], y[k], q[0]);
-            q[1] = __ffma2_rn(__fmul2_rn(dn[k], w[k]), y[k], q[1]);
-          }
-        }
-        if constexpr (POST) {
-          float2 f[P];
-          lds<E>(st.at(KF) + c * sizeof(E), f);
-#pragma unroll
-          for (int k = 0; k < P; ++k) q[2] = __ffma2_rn(f[k], f[k], q[2]);
-        }
-      }
-    }
-    float v[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
-    if constexpr (PRE || POST) row_sum_w(v, W, wi, gi, buf, flip);
-    const float sy = poison / sqrtf(fmaf(v[0], a.inv_d, a.eps));
-    const float my = v[1] * sy * a.inv_d;                  // mean(w_pre dn yh)
-    const float sf = POST ? 1.f / sqrtf(fmaf(v[2], a.inv_d, a.eps)) : 1.f;
-    float2 m2v = two(0.f);
-    float2 G[NV][P];
+    // the row into registers, with the sums of y^2, w_pre dn y and f^2
+    float2 q[3] = {two(0.f), two(0.f), two(0.f)};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 + lane) * VEC;
       if (c < st.n) {
         lds<E>(st.at(0) + c * sizeof(E), G[i]);
-#pragma unroll
-        for (int k = 0; k < P; ++k)
-          G[i][k] = make_float2(a.dy ? G[i][k].x : 0.f, a.dy ? G[i][k].y : 0.f);
         if constexpr (PRE) {
-          float2 y[P], dn[P], w[P];
-          lds<E>(st.at(KY) + c * sizeof(E), y);
-          lds<E>(st.at(KN) + c * sizeof(E), dn);
+          float2 w[P];
+          lds<E>(st.at(KY) + c * sizeof(E), y[i]);
+          lds<E>(st.at(KN) + c * sizeof(E), dn[i]);
           weights2<P>(a.w_pre, col0 + c, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
-            const float2 yh = __fmul2_rn(y[k], two(sy));
-            G[i][k] = __ffma2_rn(two(sy), __ffma2_rn(yh, two(-my), __fmul2_rn(dn[k], w[k])), G[i][k]);
-            apre[i][k] = __ffma2_rn(dn[k], yh, apre[i][k]);
+            q[0] = __ffma2_rn(y[i][k], y[i][k], q[0]);
+            q[1] = __ffma2_rn(__fmul2_rn(dn[i][k], w[k]), y[i][k], q[1]);
+          }
+        }
+        if constexpr (BLOCK) lds<E>(st.at(KF) + c * sizeof(E), f[i]);
+        if constexpr (POST)
+#pragma unroll
+          for (int k = 0; k < P; ++k) q[2] = __ffma2_rn(f[i][k], f[i][k], q[2]);
+        if constexpr (GATE == GDPA_GATE_TOKEN) {
+          lds<E>(st.at(KZ) + c * sizeof(E), z[i]);
+          act(z[i], a.sigmoid);
+        }
+      }
+    }
+    st.next(t, lane);
+    float v[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
+    if constexpr (PRE || POST) row_sum_w(v, W, wi, gi, buf, flip);
+    const float sy = poison * rsqrtf(fmaf(v[0], a.inv_d, a.eps));
+    const float my = v[1] * sy * a.inv_d;                  // mean(w_pre dn yh)
+    const float sf = POST ? rsqrtf(fmaf(v[2], a.inv_d, a.eps)) : 1.f;
+    float2 m2v = two(0.f);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 + lane) * VEC;
+      if (c < st.n) {
+        if (!a.dy)
+#pragma unroll
+          for (int k = 0; k < P; ++k) G[i][k] = two(0.f);
+        if constexpr (PRE) {
+          float2 w[P];
+          weights2<P>(a.w_pre, col0 + c, w);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            const float2 yh = __fmul2_rn(y[i][k], two(sy));
+            G[i][k] = __ffma2_rn(two(sy), __ffma2_rn(yh, two(-my), __fmul2_rn(dn[i][k], w[k])), G[i][k]);
+            apre[i][k] = __ffma2_rn(dn[i][k], yh, apre[i][k]);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(poison));
         }
         put<E>(a.dx, t * a.d + col0 + c, G[i]);
+        if constexpr (BLOCK)           // from here on G holds alpha G, then alpha act w_post G; f holds fh
+#pragma unroll
+          for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(a.alpha));
         if constexpr (POST) {
-          float2 f[P], z[P], w[P];
-          lds<E>(st.at(KF) + c * sizeof(E), f);
-          if constexpr (GATE != GDPA_GATE_NONE) gate_at(c, z);
-          weights2<P>(a.w_post, col0 + c, w);
+          float2 w[P];
+          if constexpr (!SHARED) weights2<P>(a.w_post, col0 + c, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
-            const float2 fh = __fmul2_rn(f[k], two(sf));
-            float2 du = __fmul2_rn(two(a.alpha), G[i][k]);
-            if constexpr (GATE != GDPA_GATE_NONE) du = __fmul2_rn(z[k], du);
-            const float2 e = __fmul2_rn(du, fh);
-            apost[i][k] = __fadd2_rn(apost[i][k], e);
-            m2v = __ffma2_rn(e, w[k], m2v);
+            f[i][k] = __fmul2_rn(f[i][k], two(sf));
+            const float2 e = __fmul2_rn(G[i][k], f[i][k]);
+            if constexpr (SHARED) {
+              agate[i][k] = __fadd2_rn(agate[i][k], e);
+              m2v = __ffma2_rn(e, z[i][k], m2v);
+              G[i][k] = __fmul2_rn(G[i][k], z[i][k]);
+            } else {
+              float2 ez = e;
+              if constexpr (GATE == GDPA_GATE_TOKEN) ez = __fmul2_rn(e, z[i][k]);
+              apost[i][k] = __fadd2_rn(apost[i][k], ez);
+              m2v = __ffma2_rn(ez, w[k], m2v);
+              G[i][k] = __fmul2_rn(G[i][k], w[k]);
+            }
           }
         }
       }
@@ -444,36 +491,25 @@ norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
     float m2[1] = {m2v.x + m2v.y};
     if constexpr (POST) row_sum_w(m2, W, wi, gi, buf, flip);
     const float mf = m2[0] * a.inv_d;
-    if constexpr (BLOCK) {
+    if constexpr (BLOCK)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * 32 + lane) * VEC;
         if (c < st.n) {
-          float2 f[P], z[P], w[P];
-          lds<E>(st.at(KF) + c * sizeof(E), f);
-          if constexpr (POST) weights2<P>(a.w_post, col0 + c, w);
-          if constexpr (GATE != GDPA_GATE_NONE) gate_at(c, z);
+          float2 dz[P];
 #pragma unroll
           for (int k = 0; k < P; ++k) {
-            const float2 fh = POST ? __fmul2_rn(f[k], two(sf)) : f[k];
-            const float2 gw = __fmul2_rn(POST ? __fmul2_rn(G[i][k], w[k]) : G[i][k], two(a.alpha));
-            float2 wd = gw;
-            if constexpr (GATE != GDPA_GATE_NONE) {
-              const float2 gu = __fmul2_rn(gw, fh);                     // alpha G u
-              wd = __fmul2_rn(gw, z[k]);
-              if constexpr (SHARED)
-                agate[i][k] = __fadd2_rn(agate[i][k], gu);
-              else
-                z[k] = __fmul2_rn(gu, slope(z[k]));
-            }
-            f[k] = POST ? __fmul2_rn(two(sf), __ffma2_rn(fh, two(-mf), wd)) : wd;
+            if constexpr (GATE == GDPA_GATE_TOKEN)                      // alpha G u act'
+              dz[k] = __fmul2_rn(__fmul2_rn(G[i][k], f[i][k]), slope(z[i][k]));
+            if constexpr (SHARED && !POST)
+              agate[i][k] = __ffma2_rn(G[i][k], f[i][k], agate[i][k]);
+            if constexpr (GATE == GDPA_GATE_TOKEN || (SHARED && !POST)) G[i][k] = __fmul2_rn(G[i][k], z[i][k]);
+            if constexpr (POST) G[i][k] = __fmul2_rn(two(sf), __ffma2_rn(f[i][k], two(-mf), G[i][k]));
           }
-          put<E>(a.df, t * a.d + col0 + c, f);
-          if constexpr (GATE == GDPA_GATE_TOKEN) put<E>(a.dgate, t * a.d + col0 + c, z);
+          put<E>(a.df, t * a.d + col0 + c, G[i]);
+          if constexpr (GATE == GDPA_GATE_TOKEN) put<E>(a.dgate, t * a.d + col0 + c, dz);
         }
       }
-    }
-    st.next(t, lane);
   }
   if (SHARED && st.t1 > st.t0) flush();
   // the block's weight gradients: its groups in order, through shared memory (every copy has been read)
@@ -482,7 +518,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
   for (int which = 0; which < 2; ++which) {
     float* out = which ? a.part_pre : a.part_post;
     if (!out) continue;
-    for (int r = 0; r < kWarpsS / W; ++r) {
+    for (int r = 0; r < (int)blockDim.x / 32 / W; ++r) {
       if (gi == r)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -490,19 +526,19 @@ norm_stream_bwd_kernel(const NormArgs a, int W, int stages) {
           if (c < st.n)
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-              const float2 v = which ? apre[i][k] : apost[i][k];
+              const float2 v = which ? apre[i][k] : SHARED ? spost[c / 2 + k] : apost[SHARED ? 0 : i][k];
               float2* at = reinterpret_cast<float2*>(sums + col0 + c) + k;
               *at = r == 0 ? v : __fadd2_rn(*at, v);
             }
         }
       __syncthreads();
     }
-    for (int c = threadIdx.x; c < a.d; c += kThreadsS) out[(int64_t)blockIdx.x * a.d + c] = sums[c];
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) out[(int64_t)blockIdx.x * a.d + c] = sums[c];
     __syncthreads();
   }
 }
 
-using Kernel = void (*)(const NormArgs, int, int);
+using Kernel = void (*)(const NormArgs, int);
 
 template <typename E, int NV, bool BACKWARD, bool PRE, bool POST, int GATE>
 Kernel kernel_of() {
@@ -550,20 +586,21 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   while (nv < most && nv * 32 * vec < d) nv *= 2;
   int w = 1;
   while (w * nv * 32 * vec < d) w *= 2;
-  if (w > kWarpsS) return p;
-  const int64_t groups = (int64_t)device_sm_count() * (kWarpsS / w);
+  const int warps = (backward ? kWarpsBwd : kWarpsFwd) / w * w;
+  if (warps == 0) return p;
+  const int64_t groups = (int64_t)device_sm_count() * (warps / w);
   // a range of a few rows at least: below that the registers' form has its first rows sooner
   if (T < 4 * groups) return p;
-  const uint32_t row = (uint32_t)(nv * 32 * vec * es) * tensors;
-  int stages = (int)(kRingBytes / kWarpsS / row);
-  if (stages < 2) return p;
+  const uint32_t row = (uint32_t)(nv * 32 * vec * es) * tensors * warps;   // of every warp
+  if (kStages * row > kRingBytes) return p;
   p.nv = nv;
   p.warps_row = w;
-  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  p.warps = warps;
   p.groups = (int)groups;
   p.blocks = device_sm_count();
-  p.smem = (size_t)p.stages * row * kWarpsS;
+  p.smem = (size_t)kStages * row;
   if (backward && p.smem < (size_t)d * 4) p.smem = (size_t)d * 4;
+  if (backward && gate_kind == GDPA_GATE_SAMPLE) p.smem += (size_t)warps * nv * 32 * vec * 4;   // w_post's sums
   return p;
 }
 
@@ -575,7 +612,7 @@ cudaError_t launch_norm_stream(const NormArgs& a, const StreamPlan& p, int dtype
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   if (e != cudaSuccess) return e;
   KernelScope ks_(backward ? "gdpa_block_norm_bwd" : "gdpa_block_norm_fwd", st);
-  kern<<<p.blocks, kThreadsS, p.smem, st>>>(a, p.warps_row, p.stages);
+  kern<<<p.blocks, p.warps * 32, p.smem, st>>>(a, p.warps_row);
   return cudaGetLastError();
 }
 
