@@ -683,7 +683,8 @@ cudaError_t launch_tiles(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t
   const CUtensorMapSwizzle sw = DH < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (!chunk_maps(a, c, DH, C::CH, kBNT, sw, &mq, &mk, &mv)) return cudaErrorInvalidValue;
   auto kern = chunk_tiles_kernel<DH>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kern, (int)C::SMEM, done);
   if (e != cudaSuccess) return e;
   KernelScope ks_("gdpa_chunk_tiles", st);
   kern<<<a.workers, kThreadsT, C::SMEM, st>>>(mq, mk, mv, a);

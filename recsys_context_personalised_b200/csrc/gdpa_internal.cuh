@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdpa.h"
 
 namespace gdpa {
@@ -109,6 +111,17 @@ cudaError_t launch_bias_prep(const gdpa_problem_t& p, const int32_t* offsets, co
 void reset_launch_count();
 // SMs of the current device.
 int device_sm_count();
+// Allows `kern` `bytes` of dynamic shared memory, once per device (`done`: a bit for each of the first 64).
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 64;
+  cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 // Checks a paged cache's description for a call on B samples.
 gdpa_status_t check_cache(const gdpa_cache_t* c, int32_t B);
 inline int log2_int(int x) {

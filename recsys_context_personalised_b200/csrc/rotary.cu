@@ -281,9 +281,12 @@ gdpa_status_t check_spec(const gdpa_rotary_t* r, int32_t dh) {
 // one that makes fewer than `low` is divided by `factor`, linearly in between.
 void rotary_frequencies(const gdpa_rotary_t& r, uint64_t (&turn)[64]) {
   const long double two_pi = 6.283185307179586476925286766559L;
-  for (int i = 0; i < r.rot / 2; ++i) {
-    long double w = powl((long double)r.base, -2.0L * i / r.rot);
-    long double keep = 0.0L;
+  // (by repeated multiplication: 63 roundings of 2^-64, nothing beside the 2^-64 turns of the result, where
+  // a power for every pair would take longer than the kernel on a few tokens)
+  const long double step = powl((long double)r.base, -2.0L / r.rot);
+  long double power = 1.0L;
+  for (int i = 0; i < r.rot / 2; ++i, power *= step) {
+    long double w = power, keep = 0.0L;
     if (r.trained_len > 0) {
       keep = (r.trained_len * w / two_pi - r.low) / ((long double)r.high - r.low);
       keep = keep < 0.0L ? 0.0L : keep > 1.0L ? 1.0L : keep;

@@ -8,6 +8,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -424,30 +425,41 @@ def _need(ok, where: str, what: str) -> None:
 
 def _operand(where, name, t, dtype, shape, device) -> None:
     """A contiguous tensor of that type and shape on `device`."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
-            and tuple(t.shape) == shape and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
         raise GdpaError(1, f"{where} ({name}: a contiguous {dtype} tensor {list(shape)} on {device})")
 
 
 def _heads(where, name, t, dtype, shape, device) -> int:
     """A [T, h, dh] tensor whose heads are contiguous; returns its token stride."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.device == device
-            and t.dim() == 3 and tuple(t.shape) == shape and t.stride(2) == 1
-            and (t.stride(1) == shape[2] or shape[1] == 1)):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device):
         raise GdpaError(1, f"{where} ({name}: {dtype} {list(shape)} on {device}, heads contiguous)")
-    return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+    row, head, one = t.stride()
+    if one != 1 or (head != shape[2] and shape[1] != 1):
+        raise GdpaError(1, f"{where} ({name}: {dtype} {list(shape)} on {device}, heads contiguous)")
+    return row if shape[0] > 1 else shape[1] * shape[2]
+
+
+# The current device and its current stream without the Python objects around them (of which a
+# call on one token would spend a tenth of its time).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 class _On:
     """Makes a tensor's device current, and `stream` (when given) the stream
-    that allocations belong to, for the length of a call."""
+    that allocations belong to, for the length of a call; gives the stream's handle."""
+    __slots__ = ("dev", "ctx")
 
     def __init__(self, where, t, stream):
         _need(isinstance(t, torch.Tensor) and t.is_cuda, where, "a CUDA tensor")
-        self.raw = None
-        self.ctx = []
-        if t.device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(t.device))
+        self.dev = t.get_device()
+        self.ctx = ()
+        if stream is None and self.dev == _current_device():
+            return
+        self.ctx = [torch.cuda.device(self.dev)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -457,7 +469,7 @@ class _On:
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.dev)
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
@@ -568,6 +580,12 @@ def chunk_workspace_bytes(cache: Cache, B: int, hq: int, T: int, max_n: int) -> 
     return n.value
 
 
+@functools.lru_cache(maxsize=256)
+def _chunk_workspace(device: int, hk: int, dh: int, hq: int, max_n: int) -> int:
+    """What gdpa_chunk_workspace_size says for these sizes (the others do not enter it) on the current device."""
+    return chunk_workspace_bytes(Cache(256, 256, 256, 1, 1, 16, hk, dh, 0), 1, hq, 0, max_n)
+
+
 def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, scale: float,
               max_n: int, window: Optional[int] = None, o=None, lse=None, ws=None,
               want_lse: bool = True, stream=None):
@@ -595,7 +613,7 @@ def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, sc
         elif want_lse:
             lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
         if ws is None:
-            ws = workspace(chunk_workspace_bytes(c, B, hq, T, max_n), dev)
+            ws = workspace(_chunk_workspace(dev.index, c.hk, c.dh, hq, max_n), dev)
         else:
             _need(ws.is_cuda and ws.device == dev and ws.dtype == torch.uint8
                   and ws.is_contiguous(), w, "ws: a contiguous uint8 tensor on the device")
