@@ -184,13 +184,13 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
     col[i] = (i * tpr + tid) * VEC;
     in[i] = col[i] < a.d;
   }
-  float apost[NV][VEC], apre[NV][VEC], agate[NV][VEC], gs[NV][VEC];
+  float apost[NV][VEC], apre[NV][VEC], agate[NV][VEC], gs[NV][VEC], slope[NV][VEC];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
       apost[i][k] = apre[i][k] = agate[i][k] = 0.f;
-      gs[i][k] = 1.f;
+      gs[i][k] = slope[i][k] = 1.f;
     }
   R ry[NV] = {}, rf[NV] = {}, rz[NV] = {}, rdy[NV] = {}, rdn[NV] = {};
   auto fetch = [&](int64_t row) {
@@ -226,8 +226,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
       if (in[i])
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-          const float slope = a.sigmoid ? gs[i][k] * (1.f - gs[i][k]) : 1.f;
-          out[col[i] + k] = agate[i][k] * slope * a.alpha;
+          out[col[i] + k] = agate[i][k] * slope[i][k] * a.alpha;
           agate[i][k] = 0.f;
         }
   };
@@ -243,9 +242,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
       rdn[i].get(dn[i]);
       if (a.gate_kind == GDPA_GATE_TOKEN) {
         rz[i].get(gs[i]);
-        if (a.sigmoid)
 #pragma unroll
-          for (int k = 0; k < VEC; ++k) gs[i][k] = logistic(gs[i][k]);
+        for (int k = 0; k < VEC; ++k) gate_slope(gs[i][k], a.sigmoid, gs[i][k], slope[i][k]);
       }
     }
     bool live = t < t1;
@@ -261,9 +259,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
               R r;
               r.load(a.gate, (int64_t)walk.b * a.d + col[i]);
               r.get(gs[i]);
-              if (a.sigmoid)
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) gs[i][k] = logistic(gs[i][k]);
+              for (int k = 0; k < VEC; ++k) gate_slope(gs[i][k], a.sigmoid, gs[i][k], slope[i][k]);
             }
       }
       live = walk.live(a);
@@ -326,7 +323,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         const float gu = G[i][k] * f[i][k] * w[k];          // G u
-        dz[k] = a.alpha * gu * (a.sigmoid ? gs[i][k] * (1.f - gs[i][k]) : 1.f);
+        dz[k] = a.alpha * gu * slope[i][k];
         if (a.gate_kind == GDPA_GATE_SAMPLE) agate[i][k] += gu;
         const float wd = w[k] * (a.alpha * gs[i][k] * G[i][k]);
         f[i][k] = a.w_post ? sf * fmaf(-f[i][k], mf, wd) : wd;

@@ -31,6 +31,17 @@ __device__ __forceinline__ float logistic(float z) {
   return r;
 }
 
+// act(z) and act'(z).  From t = exp(-|z|), so that the slope keeps its relative precision where act is close
+// to 1 (act (1 - act) of a rounded act loses it).
+__device__ __forceinline__ void gate_slope(float z, int sigmoid, float& act, float& slope) {
+  float t, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fabsf(z) * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + t));
+  const float s = t * r;                     // 1 / (1 + exp(|z|))
+  act = sigmoid ? (z >= 0.f ? r : s) : z;
+  slope = sigmoid ? s * r : 1.f;
+}
+
 // VEC consecutive elements of a row as floats (VEC * sizeof(E) = 16, or one element)
 template <typename E, int VEC> struct Raw;
 template <> struct Raw<__nv_bfloat16, 8> {

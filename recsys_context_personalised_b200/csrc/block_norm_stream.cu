@@ -38,42 +38,112 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// 16 bytes of shared memory as pairs of floats (the arithmetic is in packed pairs: half the instructions)
-template <typename E>
-__device__ __forceinline__ void lds(uint32_t addr, float2* f) {
-  uint32_t w[4];
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-               : "r"(addr));
-  if constexpr (sizeof(E) == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      f[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+// Which columns of a warp's segment a thread holds, and how they are read and written.  AL (rows of whole
+// 16-byte units): vector i of a thread is VEC neighbouring columns.  Otherwise rows start at any element: the
+// VEC columns lie 32 apart, so that a warp's access is contiguous, and each is tested against the segment's
+// end; a column past it reads as 0.  Values come in pairs, for the packed arithmetic.
+template <typename E, bool AL>
+struct Cols {
+  static constexpr int VEC = 16 / sizeof(E), P = VEC / 2;
+
+  // does vector i hold any column (of this thread, AL; of the warp) below n
+  static __device__ __forceinline__ bool any(int i, int lane, int n) {
+    return AL ? (i * 32 + lane) * VEC < n : i * 32 * VEC < n;
   }
-}
-template <int P>
-__device__ __forceinline__ void weights2(const float* w, int col, float2 (&f)[P]) {
-#pragma unroll
-  for (int k = 0; k < P; k += 2) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(w + col + 2 * k));
-    f[k] = make_float2(v.x, v.y);
-    f[k + 1] = make_float2(v.z, v.w);
+  static __device__ __forceinline__ int col(int i, int lane, int k) {
+    return AL ? (i * 32 + lane) * VEC + k : (i * VEC + k) * 32 + lane;
   }
-}
-template <typename E, int P>
-__device__ __forceinline__ void put(void* p, int64_t i, const float2 (&f)[P]) {
-  Raw<E, 2 * P>::store(p, i, reinterpret_cast<const float*>(f));
-}
-template <typename E, int P>
-__device__ __forceinline__ void get(const void* p, int64_t i, float2 (&f)[P]) {
-  Raw<E, 2 * P> r;
-  r.load(p, i);
-  r.get(reinterpret_cast<float*>(f));
-}
+  template <typename F>
+  static __device__ __forceinline__ void each(int i, int lane, int n, float2 (&f)[P], F read) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int c = col(i, lane, 2 * k), d = col(i, lane, 2 * k + 1);
+      f[k] = make_float2(c < n ? read(c) : 0.f, d < n ? read(d) : 0.f);
+    }
+  }
+  // from shared memory: `addr` of the segment's first element
+  static __device__ __forceinline__ void shared(uint32_t addr, int i, int lane, int n, float2 (&f)[P]) {
+    if constexpr (AL) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "r"(addr + (i * 32 + lane) * 16));
+      if constexpr (sizeof(E) == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          f[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          f[k] = make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+      }
+    } else {
+      each(i, lane, n, f, [&](int c) -> float {
+        if constexpr (sizeof(E) == 2) {
+          uint16_t v;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr + c * 2));
+          return __uint_as_float((uint32_t)v << 16);
+        } else {
+          float v;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr + c * 4));
+          return v;
+        }
+      });
+    }
+  }
+  // fp32 weights of the segment
+  static __device__ __forceinline__ void weights(const float* w, int i, int lane, int n, float2 (&f)[P]) {
+    if constexpr (AL) {
+#pragma unroll
+      for (int k = 0; k < P; k += 2) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(w + (i * 32 + lane) * VEC + 2 * k));
+        f[k] = make_float2(v.x, v.y);
+        f[k + 1] = make_float2(v.z, v.w);
+      }
+    } else {
+      each(i, lane, n, f, [&](int c) { return __ldg(w + c); });
+    }
+  }
+  static __device__ __forceinline__ void global(const E* p, int i, int lane, int n, float2 (&f)[P]) {
+    if constexpr (AL) {
+      Raw<E, VEC> r;
+      r.load(p, (i * 32 + lane) * VEC);
+      r.get(reinterpret_cast<float*>(f));
+    } else {
+      each(i, lane, n, f, [&](int c) { return Elem<E>::to_f(__ldg(p + c)); });
+    }
+  }
+  static __device__ __forceinline__ void put(E* p, int i, int lane, int n, const float2 (&f)[P]) {
+    if constexpr (AL) {
+      Raw<E, VEC>::store(p, (i * 32 + lane) * VEC, reinterpret_cast<const float*>(f));
+    } else {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int c = col(i, lane, 2 * k), d = col(i, lane, 2 * k + 1);
+        if (c < n) p[c] = Elem<E>::from_f(f[k].x);
+        if (d < n) p[d] = Elem<E>::from_f(f[k].y);
+      }
+    }
+  }
+  static __device__ __forceinline__ void each_at(const float* p, int i, int lane, int n, float2 (&f)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int c = col(i, lane, 2 * k), d = col(i, lane, 2 * k + 1);
+      f[k] = make_float2(AL || c < n ? p[c] : 0.f, AL || d < n ? p[d] : 0.f);
+    }
+  }
+  // fp32 sums, in shared or global memory: v <- op(v, f)
+  template <typename F>
+  static __device__ __forceinline__ void sums(float* p, int i, int lane, int n, const float2 (&f)[P], F op) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      const int c = col(i, lane, 2 * k), d = col(i, lane, 2 * k + 1);
+      if (AL || c < n) p[c] = op(p[c], f[k].x);
+      if (AL || d < n) p[d] = op(p[d], f[k].y);
+    }
+  }
+};
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 // act of the gate, by selection
 template <int P>
 __device__ __forceinline__ void act(float2 (&z)[P], int sigmoid) {
@@ -81,29 +151,43 @@ __device__ __forceinline__ void act(float2 (&z)[P], int sigmoid) {
   for (int k = 0; k < P; ++k)
     z[k] = make_float2(sigmoid ? logistic(z[k].x) : z[k].x, sigmoid ? logistic(z[k].y) : z[k].y);
 }
-__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+// act in place, and its slope
+template <int P>
+__device__ __forceinline__ void act(float2 (&z)[P], int sigmoid, float2 (&slope)[P]) {
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    gate_slope(z[k].x, sigmoid, z[k].x, slope[k].x);
+    gate_slope(z[k].y, sigmoid, z[k].y, slope[k].y);
+  }
+}
 
 // The rows of one warp: its columns [col0, col0 + n) of the group's rows [t0, t1), NT tensors, in a
-// ring of kStages rows.
-template <typename E, int NV, int NT>
+// ring of kStages rows.  A copy takes whole 16-byte units: of rows that start anywhere (not AL) the units around
+// them, of the tensors' last bytes those that make a whole unit, and the rest by plain loads.
+template <typename E, int NV, int NT, bool AL>
 struct Stream {
   static constexpr int VEC = 16 / sizeof(E), SEG = NV * 32 * VEC;
-  static constexpr uint32_t SEGB = SEG * sizeof(E), ROWB = NT * SEGB;
-  const E* src[NT];
+  static constexpr uint32_t SEGB = SEG * sizeof(E) + (AL ? 0 : 32), ROWB = NT * SEGB;
+  const E* src[NT];             // the tensors
   uint32_t ring, bar;
-  int64_t t0, t1;
-  int d, n, stage;
+  int64_t t0, t1, whole;        // whole: bytes of a tensor in whole units
+  int d, col0, n, stage;
   uint32_t phase;
   volatile int* abort_flag;
 
+  __device__ __forceinline__ int64_t first(int64_t t) const { return (t * d + col0) * (int64_t)sizeof(E); }
   __device__ __forceinline__ void issue(int64_t t, int slot, int lane) {
     if (t < t1 && lane == 0) {
-      const uint32_t bytes = (uint32_t)n * sizeof(E);
+      const int64_t b0 = first(t), b1 = b0 + n * (int)sizeof(E);
+      const int64_t a0 = AL ? b0 : b0 & ~(int64_t)15;
+      const int64_t a1 = AL ? b1 : min((b1 + 15) & ~(int64_t)15, whole);
+      const uint32_t bytes = n > 0 && a1 > a0 ? (uint32_t)(a1 - a0) : 0u;
       mbar_expect_tx(bar + 8 * slot, bytes * NT);
-      if (n > 0)
+      if (bytes > 0)
 #pragma unroll
         for (int k = 0; k < NT; ++k)
-          bulk_load(ring + slot * ROWB + k * SEGB, src[k] + t * d, bytes, bar + 8 * slot);
+          bulk_load(ring + slot * ROWB + k * SEGB, reinterpret_cast<const char*>(src[k]) + a0, bytes,
+                    bar + 8 * slot);
     }
   }
   __device__ __forceinline__ void start(int lane) {
@@ -111,12 +195,31 @@ struct Stream {
     phase = 0;
     for (int s = 0; s < kStages; ++s) issue(t0 + s, s, lane);
   }
-  // Waits for the current row; false (its values are garbage) when the wait ran out.
-  __device__ __forceinline__ bool wait() {
+  // Waits for row t, the current one; false (its values are garbage) when the wait ran out.
+  __device__ __forceinline__ bool wait(int64_t t, int lane) {
     const bool ok = mbar_wait(bar + 8 * stage, phase, abort_flag, kNormTimeoutNs);
+    if (!AL) {
+      base = (uint32_t)(first(t) & 15);
+      const int64_t b0 = first(t), b1 = b0 + n * (int)sizeof(E);
+      if (b1 > whole) {                            // (the last row's last few elements)
+        const int c = (int)((max(whole, b0) - b0) / (int)sizeof(E)) + lane;
+        if (c < n)
+#pragma unroll
+          for (int k = 0; k < NT; ++k) {
+            const E v = src[k][t * d + col0 + c];
+            const uint32_t to = at(k) + c * sizeof(E);
+            if constexpr (sizeof(E) == 2)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(*reinterpret_cast<const uint16_t*>(&v)) : "memory");
+            else
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"((float)v) : "memory");
+          }
+        __syncwarp();
+      }
+    }
     return __all_sync(0xffffffffu, ok);
   }
-  __device__ __forceinline__ uint32_t at(int k) const { return ring + stage * ROWB + k * SEGB; }
+  uint32_t base = 0;            // of the row's first element in the copied units
+  __device__ __forceinline__ uint32_t at(int k) const { return ring + stage * ROWB + k * SEGB + base; }
   // The current row (t) has been read: its place takes a later one.
   __device__ __forceinline__ void next(int64_t t, int lane) {
     __syncwarp();
@@ -152,11 +255,12 @@ __device__ __forceinline__ void row_sum_w(float (&v)[K], int W, int wi, int gi, 
 
 // What a call has is fixed at compile time (GATE: a gdpa_gate_t): branches on it inside the row would
 // make the compiler move the row's registers around.
-template <typename E, int NV, bool BLOCK, bool POST, int GATE>
+template <typename E, int NV, bool AL, bool BLOCK, bool POST, int GATE>
 __global__ void __launch_bounds__(kWarpsFwd * 32, 1)
 norm_stream_fwd_kernel(const NormArgs a, int W) {
-  using St = Stream<E, NV, BLOCK ? (GATE == GDPA_GATE_TOKEN ? 3 : 2) : 1>;
-  constexpr int VEC = St::VEC, P = VEC / 2;
+  using St = Stream<E, NV, BLOCK ? (GATE == GDPA_GATE_TOKEN ? 3 : 2) : 1, AL>;
+  using Co = Cols<E, AL>;
+  constexpr int P = Co::P;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarpsFwd * kStages];
   __shared__ float buf[2 * 3 * kWarpsFwd];
@@ -168,12 +272,14 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
   fence_mbar_init();
   __syncthreads();
   St st;
-  const int col0 = wi * St::SEG;
-  st.n = max(0, min(St::SEG, a.d - col0));
+  const int col0 = wi * St::SEG, n = max(0, min(St::SEG, a.d - col0));
+  st.col0 = col0;
+  st.n = n;
   st.d = a.d;
-  st.src[0] = reinterpret_cast<const E*>(a.x) + col0;
-  if constexpr (BLOCK) st.src[1] = reinterpret_cast<const E*>(a.f) + col0;
-  if constexpr (GATE == GDPA_GATE_TOKEN) st.src[2] = reinterpret_cast<const E*>(a.gate) + col0;
+  st.whole = a.T * a.d * (int64_t)sizeof(E) & ~(int64_t)15;
+  st.src[0] = reinterpret_cast<const E*>(a.x);
+  if constexpr (BLOCK) st.src[1] = reinterpret_cast<const E*>(a.f);
+  if constexpr (GATE == GDPA_GATE_TOKEN) st.src[2] = reinterpret_cast<const E*>(a.gate);
   st.ring = smem_u32(smem) + warp * (kStages * St::ROWB);
   st.bar = smem_u32(&bars[warp * kStages]);
   st.abort_flag = &abort_s;
@@ -185,7 +291,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
   walk.next = -1;
   walk.b = 0;
   for (int64_t t = st.t0; t < st.t1; ++t) {
-    const float poison = st.wait() ? 1.f : NAN;
+    const float poison = st.wait(t, lane) ? 1.f : NAN;
     float2 y[NV][P];
     bool live = true;
     if constexpr (BLOCK) {
@@ -194,10 +300,9 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
         float2 q[2] = {two(0.f), two(0.f)};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (i * 32 + lane) * VEC;
-          if (c < st.n) {
+          if (Co::any(i, lane, n)) {
             float2 f[P];
-            lds<E>(st.at(1) + c * sizeof(E), f);
+            Co::shared(st.at(1), i, lane, n, f);
 #pragma unroll
             for (int k = 0; k < P; ++k) q[k & 1] = __ffma2_rn(f[k], f[k], q[k & 1]);
           }
@@ -212,37 +317,35 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * 32 + lane) * VEC;
-        if (c < st.n) {
+        if (Co::any(i, lane, n)) {
           float2 f[P], w[P];
-          lds<E>(st.at(0) + c * sizeof(E), y[i]);
-          lds<E>(st.at(1) + c * sizeof(E), f);
+          Co::shared(st.at(0), i, lane, n, y[i]);
+          Co::shared(st.at(1), i, lane, n, f);
 #pragma unroll
           for (int k = 0; k < P; ++k) f[k] = __fmul2_rn(f[k], two(scale));
           if constexpr (POST) {
-            weights2<P>(a.w_post, col0 + c, w);
+            Co::weights(a.w_post + col0, i, lane, n, w);
 #pragma unroll
             for (int k = 0; k < P; ++k) f[k] = __fmul2_rn(f[k], w[k]);
           }
           if constexpr (GATE != GDPA_GATE_NONE) {
             if constexpr (GATE == GDPA_GATE_TOKEN)
-              lds<E>(st.at(2) + c * sizeof(E), w);
+              Co::shared(st.at(2), i, lane, n, w);
             else
-              get<E>(a.gate, (int64_t)(live ? walk.b : 0) * a.d + col0 + c, w);
+              Co::global(reinterpret_cast<const E*>(a.gate) + (int64_t)(live ? walk.b : 0) * a.d + col0, i, lane, n, w);
             act(w, a.sigmoid);
           }
 #pragma unroll
           for (int k = 0; k < P; ++k)
             y[i][k] = GATE != GDPA_GATE_NONE ? __ffma2_rn(w[k], f[k], y[i][k]) : __fadd2_rn(f[k], y[i][k]);
-          if (live) put<E>(a.y, t * a.d + col0 + c, y[i]);
+          if (live) Co::put(reinterpret_cast<E*>(a.y) + t * a.d + col0, i, lane, n, y[i]);
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * 32 + lane) * VEC;
-        if (c < st.n) {
-          lds<E>(st.at(0) + c * sizeof(E), y[i]);
+        if (Co::any(i, lane, n)) {
+          Co::shared(st.at(0), i, lane, n, y[i]);
 #pragma unroll
           for (int k = 0; k < P; ++k) y[i][k] = __fmul2_rn(y[i][k], two(poison));
         }
@@ -253,7 +356,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
       float2 q[2] = {two(0.f), two(0.f)};
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if ((i * 32 + lane) * VEC < st.n)
+        if (Co::any(i, lane, n))
 #pragma unroll
           for (int k = 0; k < P; ++k) q[k & 1] = __ffma2_rn(y[i][k], y[i][k], q[k & 1]);
       float v[1] = {(q[0].x + q[1].x) + (q[0].y + q[1].y)};
@@ -261,13 +364,12 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
       const float scale = rsqrtf(fmaf(v[0], a.inv_d, a.eps));
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * 32 + lane) * VEC;
-        if (c < st.n && live) {
+        if (Co::any(i, lane, n) && live) {
           float2 w[P];
-          weights2<P>(a.w_pre, col0 + c, w);
+          Co::weights(a.w_pre + col0, i, lane, n, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) y[i][k] = __fmul2_rn(y[i][k], __fmul2_rn(w[k], two(scale)));
-          put<E>(a.n, t * a.d + col0 + c, y[i]);
+          Co::put(reinterpret_cast<E*>(a.n) + t * a.d + col0, i, lane, n, y[i]);
         }
       }
     }
@@ -275,14 +377,15 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
 }
 
 // (A gate of GDPA_GATE_SAMPLE is one row per sample, whose gradient accumulates over the sample's rows.)
-template <typename E, int NV, bool BLOCK, bool PRE, bool POST, int GATE>
+template <typename E, int NV, bool AL, bool BLOCK, bool PRE, bool POST, int GATE>
 __global__ void __launch_bounds__(kWarpsBwd * 32, 1)
 norm_stream_bwd_kernel(const NormArgs a, int W) {
   constexpr bool SHARED = GATE == GDPA_GATE_SAMPLE;
   // the tensors, in the order dy, y, dn, f, token gate
   constexpr int KY = 1, KN = 2, KF = PRE ? 3 : 1, KZ = KF + 1;
-  using St = Stream<E, NV, KF + (BLOCK ? 1 : 0) + (GATE == GDPA_GATE_TOKEN ? 1 : 0)>;
-  constexpr int VEC = St::VEC, P = VEC / 2;
+  using St = Stream<E, NV, KF + (BLOCK ? 1 : 0) + (GATE == GDPA_GATE_TOKEN ? 1 : 0), AL>;
+  using Co = Cols<E, AL>;
+  constexpr int P = Co::P;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarpsFwd * kStages];
   __shared__ float buf[2 * 3 * kWarpsFwd];
@@ -294,16 +397,18 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
   fence_mbar_init();
   __syncthreads();
   St st;
-  const int col0 = wi * St::SEG;
-  st.n = max(0, min(St::SEG, a.d - col0));
+  const int col0 = wi * St::SEG, n = max(0, min(St::SEG, a.d - col0));
+  st.col0 = col0;
+  st.n = n;
   st.d = a.d;
-  st.src[0] = reinterpret_cast<const E*>(a.dy ? a.dy : a.dn) + col0;     // (no dy: unused)
+  st.whole = a.T * a.d * (int64_t)sizeof(E) & ~(int64_t)15;
+  st.src[0] = reinterpret_cast<const E*>(a.dy ? a.dy : a.dn);     // (no dy: unused)
   if constexpr (PRE) {
-    st.src[KY] = reinterpret_cast<const E*>(a.x) + col0;
-    st.src[KN] = reinterpret_cast<const E*>(a.dn) + col0;
+    st.src[KY] = reinterpret_cast<const E*>(a.x);
+    st.src[KN] = reinterpret_cast<const E*>(a.dn);
   }
-  if constexpr (BLOCK) st.src[KF] = reinterpret_cast<const E*>(a.f) + col0;
-  if constexpr (GATE == GDPA_GATE_TOKEN) st.src[KZ] = reinterpret_cast<const E*>(a.gate) + col0;
+  if constexpr (BLOCK) st.src[KF] = reinterpret_cast<const E*>(a.f);
+  if constexpr (GATE == GDPA_GATE_TOKEN) st.src[KZ] = reinterpret_cast<const E*>(a.gate);
   st.ring = smem_u32(smem) + warp * (kStages * St::ROWB);
   st.bar = smem_u32(&bars[warp * kStages]);
   st.abort_flag = &abort_s;
@@ -323,20 +428,16 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
   // A shared gate: agate holds the sum over the sample's rows of alpha G fh, of which both the gate's
   // gradient (times w_post act') and w_post's (times act) are made when the sample ends; the latter's sum
   // stays in shared memory between samples.
-  float2* const spost = reinterpret_cast<float2*>(smem + (size_t)(blockDim.x / 32) * kStages * St::ROWB +
-                                                  (size_t)warp * St::SEG * 4);
+  float* const spost = reinterpret_cast<float*>(smem + (size_t)(blockDim.x / 32) * kStages * St::ROWB) +
+                       warp * St::SEG;
   if constexpr (SHARED && POST)
-    for (int c = lane; c < St::SEG / 2; c += 32) spost[c] = two(0.f);
+    for (int c = lane; c < St::SEG; c += 32) spost[c] = 0.f;
   SampleWalk walk;
   walk.next = -1;
   walk.b = 0;
   // act(gate) of this thread's columns: of this row, or of this sample (times w_post)
   float2 z[GATE != GDPA_GATE_NONE ? NV : 1][P];
-  // act'(gate) from act(gate)
-  auto slope = [&](const float2 s) -> float2 {
-    const float2 v = __ffma2_rn(make_float2(-s.x, -s.y), s, s);
-    return make_float2(a.sigmoid ? v.x : 1.f, a.sigmoid ? v.y : 1.f);
-  };
+  float2 slope[GATE == GDPA_GATE_TOKEN ? NV : 1][P];          // act'(gate)
   // the rows of sample walk.b that this group holds are done: their gate gradient goes out whole, or as
   // a piece (slot 1 when it holds the sample's first row)
   auto flush = [&]() {
@@ -349,20 +450,22 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
                        : a.part_gate + ((int64_t)g * 2 + (lo >= st.t0 ? 1 : 0)) * a.d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * 32 + lane) * VEC;
-        if (c < st.n) {
+        if (Co::any(i, lane, n)) {
           float2 s[P], w[P];
-          get<E>(a.gate, (int64_t)walk.b * a.d + col0 + c, s);
-          act(s, a.sigmoid);
-          if constexpr (POST) weights2<P>(a.w_post, col0 + c, w);
+          Co::global(reinterpret_cast<const E*>(a.gate) + (int64_t)walk.b * a.d + col0, i, lane, n, s);
+          float2 ds[P];
+          act(s, a.sigmoid, ds);
+          if constexpr (POST) Co::weights(a.w_post + col0, i, lane, n, w);
+          float2 v[P];
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             const float2 sum = agate[i][k];
             agate[i][k] = two(0.f);
-            *reinterpret_cast<float2*>(out + col0 + c + 2 * k) =
-                __fmul2_rn(POST ? __fmul2_rn(sum, w[k]) : sum, slope(s[k]));
-            if constexpr (POST) spost[c / 2 + k] = __ffma2_rn(sum, s[k], spost[c / 2 + k]);
+            v[k] = __fmul2_rn(POST ? __fmul2_rn(sum, w[k]) : sum, ds[k]);
+            if constexpr (POST) s[k] = __fmul2_rn(sum, s[k]);
           }
+          Co::sums(out + col0, i, lane, n, v, [](float, float y) { return y; });
+          if constexpr (POST) Co::sums(spost, i, lane, n, s, [](float x, float y) { return x + y; });
         }
       }
     }
@@ -379,7 +482,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
       if constexpr (GATE != GDPA_GATE_NONE) z[i][k] = two(0.f);
     }
   for (int64_t t = st.t0; t < st.t1; ++t) {
-    const float poison = st.wait() ? 1.f : NAN;
+    const float poison = st.wait(t, lane) ? 1.f : NAN;
     bool live = true;
     if constexpr (SHARED) {
       if (t >= walk.next) {
@@ -388,13 +491,12 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
         if (walk.live(a))
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
-            const int c = (i * 32 + lane) * VEC;
-            if (c < st.n) {
-              get<E>(a.gate, (int64_t)walk.b * a.d + col0 + c, z[i]);
+            if (Co::any(i, lane, n)) {
+              Co::global(reinterpret_cast<const E*>(a.gate) + (int64_t)walk.b * a.d + col0, i, lane, n, z[i]);
               act(z[i], a.sigmoid);
               if constexpr (POST) {
                 float2 w[P];
-                weights2<P>(a.w_post, col0 + c, w);
+                Co::weights(a.w_post + col0, i, lane, n, w);
 #pragma unroll
                 for (int k = 0; k < P; ++k) z[i][k] = __fmul2_rn(z[i][k], w[k]);
               }
@@ -411,27 +513,26 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
     float2 q[3] = {two(0.f), two(0.f), two(0.f)};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * 32 + lane) * VEC;
-      if (c < st.n) {
-        lds<E>(st.at(0) + c * sizeof(E), G[i]);
+      if (Co::any(i, lane, n)) {
+        Co::shared(st.at(0), i, lane, n, G[i]);
         if constexpr (PRE) {
           float2 w[P];
-          lds<E>(st.at(KY) + c * sizeof(E), y[i]);
-          lds<E>(st.at(KN) + c * sizeof(E), dn[i]);
-          weights2<P>(a.w_pre, col0 + c, w);
+          Co::shared(st.at(KY), i, lane, n, y[i]);
+          Co::shared(st.at(KN), i, lane, n, dn[i]);
+          Co::weights(a.w_pre + col0, i, lane, n, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             q[0] = __ffma2_rn(y[i][k], y[i][k], q[0]);
             q[1] = __ffma2_rn(__fmul2_rn(dn[i][k], w[k]), y[i][k], q[1]);
           }
         }
-        if constexpr (BLOCK) lds<E>(st.at(KF) + c * sizeof(E), f[i]);
+        if constexpr (BLOCK) Co::shared(st.at(KF), i, lane, n, f[i]);
         if constexpr (POST)
 #pragma unroll
           for (int k = 0; k < P; ++k) q[2] = __ffma2_rn(f[i][k], f[i][k], q[2]);
         if constexpr (GATE == GDPA_GATE_TOKEN) {
-          lds<E>(st.at(KZ) + c * sizeof(E), z[i]);
-          act(z[i], a.sigmoid);
+          Co::shared(st.at(KZ), i, lane, n, z[i]);
+          act(z[i], a.sigmoid, slope[i]);
         }
       }
     }
@@ -444,14 +545,13 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
     float2 m2v = two(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * 32 + lane) * VEC;
-      if (c < st.n) {
+      if (Co::any(i, lane, n)) {
         if (!a.dy)
 #pragma unroll
           for (int k = 0; k < P; ++k) G[i][k] = two(0.f);
         if constexpr (PRE) {
           float2 w[P];
-          weights2<P>(a.w_pre, col0 + c, w);
+          Co::weights(a.w_pre + col0, i, lane, n, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             const float2 yh = __fmul2_rn(y[i][k], two(sy));
@@ -462,13 +562,13 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
 #pragma unroll
           for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(poison));
         }
-        put<E>(a.dx, t * a.d + col0 + c, G[i]);
+        Co::put(reinterpret_cast<E*>(a.dx) + t * a.d + col0, i, lane, n, G[i]);
         if constexpr (BLOCK)           // from here on G holds alpha G, then alpha act w_post G; f holds fh
 #pragma unroll
           for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(a.alpha));
         if constexpr (POST) {
           float2 w[P];
-          if constexpr (!SHARED) weights2<P>(a.w_post, col0 + c, w);
+          if constexpr (!SHARED) Co::weights(a.w_post + col0, i, lane, n, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             f[i][k] = __fmul2_rn(f[i][k], two(sf));
@@ -494,20 +594,19 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
     if constexpr (BLOCK)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * 32 + lane) * VEC;
-        if (c < st.n) {
+        if (Co::any(i, lane, n)) {
           float2 dz[P];
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             if constexpr (GATE == GDPA_GATE_TOKEN)                      // alpha G u act'
-              dz[k] = __fmul2_rn(__fmul2_rn(G[i][k], f[i][k]), slope(z[i][k]));
+              dz[k] = __fmul2_rn(__fmul2_rn(G[i][k], f[i][k]), slope[i][k]);
             if constexpr (SHARED && !POST)
               agate[i][k] = __ffma2_rn(G[i][k], f[i][k], agate[i][k]);
             if constexpr (GATE == GDPA_GATE_TOKEN || (SHARED && !POST)) G[i][k] = __fmul2_rn(G[i][k], z[i][k]);
             if constexpr (POST) G[i][k] = __fmul2_rn(two(sf), __ffma2_rn(f[i][k], two(-mf), G[i][k]));
           }
-          put<E>(a.df, t * a.d + col0 + c, G[i]);
-          if constexpr (GATE == GDPA_GATE_TOKEN) put<E>(a.dgate, t * a.d + col0 + c, dz);
+          Co::put(reinterpret_cast<E*>(a.df) + t * a.d + col0, i, lane, n, G[i]);
+          if constexpr (GATE == GDPA_GATE_TOKEN) Co::put(reinterpret_cast<E*>(a.dgate) + t * a.d + col0, i, lane, n, dz);
         }
       }
   }
@@ -522,14 +621,16 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
       if (gi == r)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = (i * 32 + lane) * VEC;
-          if (c < st.n)
+          if (Co::any(i, lane, n)) {
+            float2 v[P];
+            if (SHARED && !which) {
+              Co::each_at(spost, i, lane, n, v);
+            } else {
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-              const float2 v = which ? apre[i][k] : SHARED ? spost[c / 2 + k] : apost[SHARED ? 0 : i][k];
-              float2* at = reinterpret_cast<float2*>(sums + col0 + c) + k;
-              *at = r == 0 ? v : __fadd2_rn(*at, v);
+              for (int k = 0; k < P; ++k) v[k] = which ? apre[i][k] : apost[SHARED ? 0 : i][k];
             }
+            Co::sums(sums + col0, i, lane, n, v, [&](float x, float y) { return r == 0 ? y : x + y; });
+          }
         }
       __syncthreads();
     }
@@ -540,37 +641,37 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
 
 using Kernel = void (*)(const NormArgs, int);
 
-template <typename E, int NV, bool BACKWARD, bool PRE, bool POST, int GATE>
+template <typename E, int NV, bool AL, bool BACKWARD, bool PRE, bool POST, int GATE>
 Kernel kernel_of() {
   if constexpr (BACKWARD)
-    return norm_stream_bwd_kernel<E, NV, true, PRE, POST, GATE>;
+    return norm_stream_bwd_kernel<E, NV, AL, true, PRE, POST, GATE>;
   else
-    return norm_stream_fwd_kernel<E, NV, true, POST, GATE>;
+    return norm_stream_fwd_kernel<E, NV, AL, true, POST, GATE>;
 }
-template <typename E, int NV, bool BACKWARD, bool PRE, bool POST>
+template <typename E, int NV, bool AL, bool BACKWARD, bool PRE, bool POST>
 Kernel kernel_of(const NormArgs& a) {
-  if (a.gate_kind == GDPA_GATE_TOKEN) return kernel_of<E, NV, BACKWARD, PRE, POST, GDPA_GATE_TOKEN>();
-  if (a.gate_kind == GDPA_GATE_SAMPLE) return kernel_of<E, NV, BACKWARD, PRE, POST, GDPA_GATE_SAMPLE>();
-  return kernel_of<E, NV, BACKWARD, PRE, POST, GDPA_GATE_NONE>();
+  if (a.gate_kind == GDPA_GATE_TOKEN) return kernel_of<E, NV, AL, BACKWARD, PRE, POST, GDPA_GATE_TOKEN>();
+  if (a.gate_kind == GDPA_GATE_SAMPLE) return kernel_of<E, NV, AL, BACKWARD, PRE, POST, GDPA_GATE_SAMPLE>();
+  return kernel_of<E, NV, AL, BACKWARD, PRE, POST, GDPA_GATE_NONE>();
 }
-template <typename E, int NV, bool BACKWARD>
+template <typename E, int NV, bool AL, bool BACKWARD>
 Kernel kernel_of(const NormArgs& a) {
   if (!a.f) {
     if constexpr (BACKWARD)
-      return norm_stream_bwd_kernel<E, NV, false, true, false, GDPA_GATE_NONE>;
+      return norm_stream_bwd_kernel<E, NV, AL, false, true, false, GDPA_GATE_NONE>;
     else
-      return norm_stream_fwd_kernel<E, NV, false, false, GDPA_GATE_NONE>;
+      return norm_stream_fwd_kernel<E, NV, AL, false, false, GDPA_GATE_NONE>;
   }
   if constexpr (BACKWARD)             // (forward, n is a test beside the row's sum)
     if (!a.w_pre)
-      return a.w_post ? kernel_of<E, NV, BACKWARD, false, true>(a) : kernel_of<E, NV, BACKWARD, false, false>(a);
-  return a.w_post ? kernel_of<E, NV, BACKWARD, true, true>(a) : kernel_of<E, NV, BACKWARD, true, false>(a);
+      return a.w_post ? kernel_of<E, NV, AL, BACKWARD, false, true>(a) : kernel_of<E, NV, AL, BACKWARD, false, false>(a);
+  return a.w_post ? kernel_of<E, NV, AL, BACKWARD, true, true>(a) : kernel_of<E, NV, AL, BACKWARD, true, false>(a);
 }
 
-template <typename E>
+template <typename E, bool AL>
 Kernel dispatch(const NormArgs& a, int nv, bool backward) {
-  if (backward) return nv == kMaxBwd ? kernel_of<E, kMaxBwd, true>(a) : kernel_of<E, kMaxBwd / 2, true>(a);
-  return nv == kMaxFwd ? kernel_of<E, kMaxFwd, false>(a) : kernel_of<E, kMaxFwd / 2, false>(a);
+  if (backward) return nv == kMaxBwd ? kernel_of<E, kMaxBwd, AL, true>(a) : kernel_of<E, kMaxBwd / 2, AL, true>(a);
+  return nv == kMaxFwd ? kernel_of<E, kMaxFwd, AL, false>(a) : kernel_of<E, kMaxFwd / 2, AL, false>(a);
 }
 
 }  // namespace
@@ -579,8 +680,8 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   StreamPlan p = {};
   const int tensors = (backward ? 4 : 2) + (gate_kind == GDPA_GATE_TOKEN ? 1 : 0);   // at most
   const int es = dtype == GDPA_DTYPE_BF16 ? 2 : 4, vec = 16 / es;
-  // rows of whole 16-byte units, at least a warp's width
-  if (d % vec || d < 32 * vec) return p;
+  const bool aligned = d % vec == 0;
+  if (d < 32 * vec) return p;                     // narrower than a warp
   const int most = backward ? kMaxBwd : kMaxFwd;
   int nv = most / 2;
   while (nv < most && nv * 32 * vec < d) nv *= 2;
@@ -591,7 +692,7 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   const int64_t groups = (int64_t)device_sm_count() * (warps / w);
   // a range of a few rows at least: below that the registers' form has its first rows sooner
   if (T < 4 * groups) return p;
-  const uint32_t row = (uint32_t)(nv * 32 * vec * es) * tensors * warps;   // of every warp
+  const uint32_t row = (uint32_t)(nv * 32 * vec * es + (aligned ? 0 : 32)) * tensors * warps;   // of every warp
   if (kStages * row > kRingBytes) return p;
   p.nv = nv;
   p.warps_row = w;
@@ -606,8 +707,11 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
 
 cudaError_t launch_norm_stream(const NormArgs& a, const StreamPlan& p, int dtype, bool backward,
                                cudaStream_t st) {
-  Kernel kern = dtype == GDPA_DTYPE_BF16 ? dispatch<__nv_bfloat16>(a, p.nv, backward)
-                                         : dispatch<float>(a, p.nv, backward);
+  const bool bf16 = dtype == GDPA_DTYPE_BF16, aligned = a.d % (bf16 ? 8 : 4) == 0;
+  Kernel kern = bf16 ? aligned ? dispatch<__nv_bfloat16, true>(a, p.nv, backward)
+                               : dispatch<__nv_bfloat16, false>(a, p.nv, backward)
+                     : aligned ? dispatch<float, true>(a, p.nv, backward)
+                               : dispatch<float, false>(a, p.nv, backward);
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   if (e != cudaSuccess) return e;

@@ -478,12 +478,14 @@ def test_norm_shared_gates(n, d):
 @pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 256), (torch.bfloat16, 776), (torch.bfloat16, 1024),
                                      (torch.bfloat16, 2056), (torch.bfloat16, 5000), (torch.bfloat16, 8192),
                                      (torch.float32, 128), (torch.float32, 1000), (torch.float32, 1540),
-                                     (torch.float32, 4096)])
+                                     (torch.float32, 4096), (torch.bfloat16, 257), (torch.bfloat16, 1001),
+                                     (torch.bfloat16, 2053), (torch.float32, 130), (torch.float32, 1001),
+                                     (torch.float32, 2047)])
 @pytest.mark.parametrize("gate,post,pre", [("token", True, True), ("sample", True, True), (None, False, True),
                                            ("sample", False, False), (None, True, False)])
 def test_norm_streamed_rows(dtype, d, gate, post, pre):
-    """Enough rows for every group of warps to walk a range: rows of one to eight warps, whole and cut last
-    segments, samples that span several groups, rows behind the last sample."""
+    """Enough rows for every group of warps to walk a range: rows of one to sixteen warps, whole and cut last
+    segments, rows that start anywhere, samples that span several groups, rows behind the last sample."""
     _check_norm([2000, 0, 1, 2900], d, dtype, gate, post, pre, seed=d, pad=7 if gate == "sample" else 0)
 
 
@@ -491,6 +493,22 @@ def test_norm_streamed_rows(dtype, d, gate, post, pre):
 def test_norm_scales(std):
     """Rows of zeros (the root holds eps alone), tiny and huge rows."""
     _check_norm([6, 5], 72, torch.float32, std=std, seed=4)
+
+
+@pytest.mark.parametrize("T,d", [(40, 72), (40, 71), (5000, 520), (5000, 519)])
+@pytest.mark.parametrize("gate", ["token", "sample"])
+def test_norm_saturated_gates(T, d, gate):
+    """Gates from -12 to 12: the slope act (1 - act) keeps its relative precision on both sides."""
+    t, rnd = _norm_case(T, d, torch.float32, gate, True, False, 9, B=2)
+    t["gate"] = torch.linspace(-12, 12, t["gate"].numel()).view_as(t["gate"])
+    dy = rnd(T, d)
+    off, sample = (None, None) if gate == "token" else (_int32([0, 7, T]), (torch.arange(T) >= 7).long())
+    got = G.block_norm_bwd(t["x"].to(DEV), t["f"].to(DEV), t["gate"].to(DEV), t["w_post"].to(DEV), None,
+                           dy.to(DEV), offsets=off, sigmoid=True)[2]
+    v, mag = ref.block_norm_grads(_dbl(t["x"]), _dbl(t["f"]), _dbl(t["gate"]), _dbl(t["w_post"]), None, _dbl(dy),
+                                  None, sample=sample, B=2, sigmoid=True)["dgate"]
+    extra = 2.0 ** -16 + (2.0 ** -24 * (T + 300) if sample is not None else 0)
+    _near(got, v.numpy(), (HALF[torch.float32] * v.abs() + extra * mag).numpy())
 
 
 def test_norm_without_a_block():
