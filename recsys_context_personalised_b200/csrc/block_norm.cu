@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_fwd_kernel(const NormArgs a, 
 
 template <typename E, int VEC, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, int tpr) {
+  pdl_trigger();
   __shared__ float buf[128];
   int flip = 0;
   using R = Raw<E, VEC>;
@@ -364,6 +365,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
 __global__ void __launch_bounds__(1024)
 norm_join_kernel(const NormArgs a, float* dw_post, float* dw_pre, int blocks) {
   __shared__ float s[32][33];
+  pdl_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   if (blockIdx.y < 2) {
     const float* part = blockIdx.y ? a.part_pre : a.part_post;
@@ -622,9 +624,9 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const i
     KernelScope ks_("gdpa_block_norm_join", st);
     const int cols = (p->d + 31) / 32;
     const int rows = p->gate == GDPA_GATE_SAMPLE ? (p->B < 1024 ? p->B : 1024) : 0;
-    norm_join_kernel<<<dim3(cols > rows ? cols : rows, p->gate == GDPA_GATE_SAMPLE ? 3 : 2), 1024,
-                       0, st>>>(a, dw_post, dw_pre, pl.blocks);
-    e = cudaGetLastError();
+    e = launch_dependent(norm_join_kernel,
+                         dim3(cols > rows ? cols : rows, p->gate == GDPA_GATE_SAMPLE ? 3 : 2), dim3(1024),
+                         st, a, dw_post, dw_pre, pl.blocks);
   }
   return finish(e);
 }

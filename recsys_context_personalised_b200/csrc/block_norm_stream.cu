@@ -380,6 +380,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
 template <typename E, int NV, bool AL, bool BLOCK, bool PRE, bool POST, int GATE>
 __global__ void __launch_bounds__(kWarpsBwd * 32, 1)
 norm_stream_bwd_kernel(const NormArgs a, int W) {
+  pdl_trigger();
   constexpr bool SHARED = GATE == GDPA_GATE_SAMPLE;
   // the tensors, in the order dy, y, dn, f, token gate
   constexpr int KY = 1, KN = 2, KF = PRE ? 3 : 1, KZ = KF + 1;

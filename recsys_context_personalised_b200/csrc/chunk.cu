@@ -723,16 +723,8 @@ bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int b
 template <int DH, int SPLIT>
 cudaError_t launch_join(const ChunkArgs& a, WsHeader* ws, cudaStream_t st) {
   KernelScope ks_("gdpa_chunk_join", st);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.workers, a.rows / 8);
-  cfg.blockDim = dim3(DH / 16 * SPLIT * 32);
-  cfg.stream = st;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<DH, SPLIT>, a, ws);
+  return launch_dependent(chunk_join_kernel<DH, SPLIT>, dim3(a.workers, a.rows / 8),
+                          dim3(DH / 16 * SPLIT * 32), st, a, ws);
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st) {
   // few items leave many pieces to each (about workers / items): 512 threads share them

@@ -143,13 +143,6 @@ bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int b
 // Many rows per sample (chunk_sm100.cu), one worker per SM.
 cudaError_t launch_chunk_tiles(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t st);
 
-// Programmatic dependent launch: the join's blocks are scheduled as this kernel's end, and wait for
-// its completion before they read anything.
-__device__ __forceinline__ void pdl_trigger() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Joins the pieces of the items that a part's border cuts, and the workers'
 // status words into the workspace's.
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st);

@@ -139,6 +139,27 @@ struct KernelScope {
   cudaStream_t st;
 };
 
+// Programmatic dependent launch: a kernel launched with launch_dependent has its blocks scheduled as the kernel
+// before it ends (from its pdl_trigger on), and waits (pdl_wait) for that one's completion before it reads
+// anything of it.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Elementwise phi of the PFFN variants on a scaled logit x, and dphi/dx:
 // ReLU max(x, 0); GELU in its exact form x * Phi(x), Phi(x) = (1 + erf(x/sqrt 2))/2,
 // with derivative Phi(x) + x * exp(-x^2/2) / sqrt(2 pi) (erf to 3.4e-6, below).
