@@ -1,6 +1,6 @@
 // The block norm on rows streamed through shared memory (formulas: block_norm.cu).
 //
-// Bound: memory, every row once.  A row belongs to one warp (or to 2, 4 or 8 where it is
+// Bound: memory, every row once.  A row belongs to one warp (or to a few where it is
 // wide), a group of warps walks a contiguous range of rows, and every warp keeps the next rows of its
 // columns in flight by bulk copies into a ring of its own: the copies need no registers, so the
 // bytes in flight (about 100 KB an SM) do not depend on what the arithmetic holds, and a row's
@@ -682,24 +682,26 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   const int tensors = (backward ? 4 : 2) + (gate_kind == GDPA_GATE_TOKEN ? 1 : 0);   // at most
   const int es = dtype == GDPA_DTYPE_BF16 ? 2 : 4, vec = 16 / es;
   const bool aligned = d % vec == 0;
-  if (d < 32 * vec) return p;                     // narrower than a warp
+  // Narrow rows fill few lanes of a warp: many of them are quicker in the registers' form, which puts several
+  // into a warp (14 k bf16 rows of 64 forward 4.3 and 8.6 us, of 130 already 21 and 11; backward 500 rows of
+  // 64 14.9 and 8.5 us, 14 k 19.8 and 18.0).  Wider rows are quicker streamed at every length (64 rows of 1024
+  // 4.0 and 3.9 us, 14 k 37 and 29).
+  if (d < 128 && (!backward || T > 8192)) return p;
   const int most = backward ? kMaxBwd : kMaxFwd;
   int nv = most / 2;
   while (nv < most && nv * 32 * vec < d) nv *= 2;
-  int w = 1;
-  while (w * nv * 32 * vec < d) w *= 2;
+  const int w = (d + nv * 32 * vec - 1) / (nv * 32 * vec);
   const int warps = (backward ? kWarpsBwd : kWarpsFwd) / w * w;
   if (warps == 0) return p;
-  const int64_t groups = (int64_t)device_sm_count() * (warps / w);
-  // a range of a few rows at least: below that the registers' form has its first rows sooner
-  if (T < 4 * groups) return p;
+  int64_t groups = (int64_t)device_sm_count() * (warps / w);
+  if (groups > T) groups = T;
   const uint32_t row = (uint32_t)(nv * 32 * vec * es + (aligned ? 0 : 32)) * tensors * warps;   // of every warp
   if (kStages * row > kRingBytes) return p;
   p.nv = nv;
   p.warps_row = w;
   p.warps = warps;
   p.groups = (int)groups;
-  p.blocks = device_sm_count();
+  p.blocks = (int)((groups + warps / w - 1) / (warps / w));
   p.smem = (size_t)kStages * row;
   if (backward && p.smem < (size_t)d * 4) p.smem = (size_t)d * 4;
   if (backward && gate_kind == GDPA_GATE_SAMPLE) p.smem += (size_t)warps * nv * 32 * vec * 4;   // w_post's sums

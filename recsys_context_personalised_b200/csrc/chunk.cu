@@ -8,14 +8,15 @@
 // head makes 2 products per loaded element, so the query heads that share a kv
 // head (and the sample's new tokens) form the 16 (or 32) rows of one tile and
 // every loaded key serves them all.  The work is cut into equal runs of
-// 64-position blocks (chunk_plan.cuh), two workers per SM.
+// blocks (chunk_plan.cuh), two workers per SM.
 //
-// A worker is a CTA of 5 warps: warp 4 loads (Q, and K and V blocks through a
-// ring of TMA slots, one copy per page piece), warps 0-3 each take 16 of a
-// block's 64 positions: S = Q K^T (mma.sync m16n8k16, which at these row counts is
+// A worker is a CTA of 5 warps: warp 4 loads (Q, and K and V blocks of 16 KB through a
+// ring of TMA slots, one copy per page piece), warps 0-3 each take 16 of every
+// 64 positions: S = Q K^T (mma.sync m16n8k16, which at these row counts is
 // far from bounding), an online softmax with running max and sum in fp32, and
-// O += P V with P rounded to bf16 (its rounding, 2^-9, is that of the output).
-// The warps' (max, sum, O) meet in shared memory at the end of the item.
+// O += P V with P rounded to bf16 (the precision of the output).
+// The warps' (max, sum, O) meet in shared memory at the end of the item, where each thread joins and
+// stores a part of the rows.
 #include <math.h>
 #include <stdio.h>
 
@@ -26,8 +27,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kBN = 64, kBNShift = 6;
-constexpr int kWarps = 4;                       // consumer warps
+constexpr int kWarps = 4, kSub = 16 * kWarps;      // consumer warps, and the positions that they take at a time
 constexpr int kThreadsC = (kWarps + 1) * 32;
 
 // What the loader tells the consumers about one block.
@@ -44,22 +44,24 @@ enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };
 template <int DH, int MT>
 struct Cfg {
   static constexpr int R = 16 * MT;                       // rows of a tile
+  static constexpr int kBN = 8192 / DH, kBNShift = chunk_rows_shift(DH);   // positions of a block (16 KB of K)
+  static_assert(1 << kBNShift == kBN, "positions of a block");
   static constexpr int CH = DH < 64 ? DH : 64;            // elements per swizzled row
   static constexpr int NCH = DH / CH;
   static constexpr uint32_t ROWB = CH * 2;
   static constexpr uint32_t SLOTB = kBN * DH * 2;         // one K or V block
   static constexpr uint32_t CHUNKB = kBN * ROWB;
   static constexpr uint32_t QB = R * DH * 2, QCHUNKB = R * ROWB;
-  static constexpr int QST = MT == 2 && DH == 128 ? 1 : 2;   // Q stages
-  static constexpr int NS = DH == 128 ? (MT == 1 ? 5 : 4) : DH == 64 ? 10 : 16;   // K/V ring slots
+  static constexpr int QST = 2;                           // Q stages
+  static constexpr int NS = DH == 128 ? 4 : DH == 64 ? (MT == 1 ? 5 : 4) : MT == 1 ? 6 : 5;   // K/V ring slots
   static constexpr int NM = 32;                           // meta ring (blocks in flight < NM)
-  // merge: two warps' O (fp32) at a time, and every warp's (max, sum)
+  // merge: every warp's O (fp32) and (max, sum)
   static constexpr uint32_t OFF_Q = 0, OFF_KV = (QST * QB + 1023) / 1024 * 1024,
-                            OFF_MRG = OFF_KV + NS * SLOTB, MRGB = 2 * R * (DH + 4) * 4,
+                            OFF_MRG = OFF_KV + NS * SLOTB, MRGB = kWarps * R * (DH + 4) * 4,
                             OFF_ML = OFF_MRG + MRGB, OFF_META = OFF_ML + kWarps * R * 8,
                             OFF_CTL = OFF_META + NM * sizeof(BlockMeta);
   static constexpr int B_KVFULL = 0, B_KVEMPTY = NS, B_QFULL = 2 * NS, B_QEMPTY = 2 * NS + QST,
-                       B_JOIN = 2 * NS + 2 * QST, NBAR = B_JOIN + 1;
+                       B_JOIN = 2 * NS + 2 * QST, B_FREE = B_JOIN + 1, NBAR = B_JOIN + 2;
   static constexpr uint32_t SMEM = 1024 + OFF_CTL + 8 * NBAR + 16;
   static_assert(SMEM <= 113 * 1024, "two workers share an SM");
   static_assert(NS / 2 + 2 < NM, "meta ring");
@@ -120,6 +122,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       mbar_init(bar(C::B_QEMPTY + i), kWarps);
     }
     mbar_init(bar(C::B_JOIN), kWarps);
+    mbar_init(bar(C::B_FREE), kWarps);
     *abort_flag = 0;
     bad_page = 0;
     fence_mbar_init();
@@ -136,8 +139,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       prefetch_tmap(&tmK);
       prefetch_tmap(&tmV);
     }
-    const int pr = min(kBN, 1 << a.page_shift);             // rows of a page piece
-    const int pieces = kBN / pr;
+    const int pr = min(C::kBN, 1 << a.page_shift);          // rows of a page piece
+    const int pieces = C::kBN / pr;
     const int heads = a.hk * a.vheads;
     int b = start.b;
     ChunkPlace at = start.at;
@@ -169,7 +172,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
         ++qn;
       }
-      const int key0 = (kb0 + at.block) << kBNShift;
+      const int key0 = (kb0 + at.block) << C::kBNShift;
       // page pieces of this block that hold a visible position: lanes 0 .. pieces - 1
       int32_t page = -1;
       bool load = false;
@@ -245,33 +248,28 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     // ----------------------------------------------------------- consumers
     const int g8 = lane >> 2, t4 = lane & 3;
     const int mat = lane >> 3, r8 = lane & 7;
-    const int kw = warp * 16;                               // this warp's positions in a block
     float o[MT][DH / 8][4];
     float mx[MT][2], sum[MT][2];
     int pos[MT][2];
-    uint32_t slot = 0, phase = 0, mslot = 0, qn = 0;
+    uint32_t slot = 0, phase = 0, mslot = 0, qn = 0, merges = 0;
     uint32_t sq = 0;
     float* mrg = reinterpret_cast<float*>(gbase + C::OFF_MRG);
     float2* mls = reinterpret_cast<float2*>(gbase + C::OFF_ML);
     bool ok = true;
-    // the consumer warps meet (bounded like every wait: a warp that gave up does not hold the others)
-    uint32_t jphase = 0;
-    auto meet = [&]() -> bool {
+    auto wait = [&](int b, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, abort_flag, kChunkTimeoutNs));
+    };
+    auto arrive = [&](int b) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_JOIN));
-      const bool all = mbar_wait(bar(C::B_JOIN), jphase, abort_flag, kChunkTimeoutNs);
-      jphase ^= 1u;
-      return __all_sync(0xffffffffu, all);
+      if (lane == 0) mbar_arrive(bar(b));
     };
     for (int64_t i = 0; i < count; ++i) {
-      ok = mbar_wait(bar(C::B_KVFULL + slot), phase, abort_flag, kChunkTimeoutNs);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (!wait(C::B_KVFULL + slot, phase)) break;
       const BlockMeta m = meta[mslot];
       if (++mslot == (uint32_t)C::NM) mslot = 0;
       if (m.flags & kFirst) {
         const uint32_t qs = qn % C::QST, qph = (qn / C::QST) & 1u;
-        ok = mbar_wait(bar(C::B_QFULL + qs), qph, abort_flag, kChunkTimeoutNs);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        if (!wait(C::B_QFULL + qs, qph)) break;
         sq = base + C::OFF_Q + qs * C::QB;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
@@ -287,245 +285,215 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             for (int x = 0; x < 4; ++x) o[mt][n][x] = 0.f;
         }
       }
-      // S = Q K^T of this warp's 16 positions
-      const uint32_t sk = base + C::OFF_KV + slot * C::SLOTB;
-      float s[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[mt][0][x] = s[mt][1][x] = 0.f;
-#pragma unroll
-      for (int k = 0; k < DH / 16; ++k) {
-        constexpr int PER = C::CH / 16;                     // 16-element steps per chunk
-        uint32_t kb[4];
-        ldsm4(unit_addr<C::CH>(sk + (k / PER) * C::CHUNKB, kw + (mat >> 1) * 8 + r8,
-                               (k % PER) * 2 + (mat & 1)), kb);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t qa[4];
-          ldsm4(unit_addr<C::CH>(sq + (k / PER) * C::QCHUNKB, mt * 16 + (mat & 1) * 8 + r8,
-                                 (k % PER) * 2 + (mat >> 1)), qa);
-          mma16816(s[mt][0], qa, kb[0], kb[1]);
-          mma16816(s[mt][1], qa, kb[2], kb[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(C::B_KVEMPTY + slot));
-        if (m.flags & kLast) mbar_arrive(bar(C::B_QEMPTY + qn % C::QST));
-      }
-      if (m.flags & kLast) ++qn;
+      const uint32_t kslot = slot;
       if (++slot == (uint32_t)C::NS) {
         slot = 0;
         phase ^= 1u;
       }
-      // online softmax; positions outside (pos - window, pos] are masked by selection
-      const int kp = m.key0 + kw + t4 * 2;                  // + 8 n + j
-      uint32_t p[MT][4];
+      const uint32_t sk = base + C::OFF_KV + kslot * C::SLOTB, sv = base + C::OFF_KV + slot * C::SLOTB;
+      bool have_v = false;
+#pragma unroll 1
+      for (int kw = warp * 16; kw < C::kBN; kw += kSub) {   // this warp's next 16 positions
+        if (m.key0 + kw >= m.hi || m.key0 + kw + 16 <= m.lo) continue;   // (no row of the tile sees one)
+        // S = Q K^T
+        float s[MT][2][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float big[2] = {-INFINITY, -INFINITY};
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+          for (int x = 0; x < 4; ++x) s[mt][0][x] = s[mt][1][x] = 0.f;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int row = x >> 1, key = kp + 8 * n + (x & 1);
-            const bool see = key <= pos[mt][row] && (int64_t)key > (int64_t)pos[mt][row] - a.window &&
-                             key >= 0;
-            s[mt][n][x] = see ? s[mt][n][x] * a.scale_log2 : -INFINITY;
-            big[row] = fmaxf(big[row], s[mt][n][x]);
-          }
+        for (int k = 0; k < DH / 16; ++k) {
+          constexpr int PER = C::CH / 16;                   // 16-element steps per chunk
+          uint32_t kb[4];
+          ldsm4(unit_addr<C::CH>(sk + (k / PER) * C::CHUNKB, kw + (mat >> 1) * 8 + r8,
+                                 (k % PER) * 2 + (mat & 1)), kb);
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-          big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 1));
-          big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 2));
-        }
-        // the running max moves only when it grew by more than 2^8 (softmax does
-        // not depend on the offset, and 2^8 is far from overflow)
-        const bool move = big[0] > mx[mt][0] + 8.f || big[1] > mx[mt][1] + 8.f;
-        if (__any_sync(0xffffffffu, move)) {
-          float f[2];
-#pragma unroll
-          for (int row = 0; row < 2; ++row) {
-            const float to = fmaxf(mx[mt][row], big[row]);
-            f[row] = to == -INFINITY ? 1.f : ex2_approx(mx[mt][row] - to);
-            mx[mt][row] = to;
-            sum[mt][row] *= f[row];
-          }
-#pragma unroll
-          for (int n = 0; n < DH / 8; ++n) {
-            o[mt][n][0] *= f[0];
-            o[mt][n][1] *= f[0];
-            o[mt][n][2] *= f[1];
-            o[mt][n][3] *= f[1];
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t qa[4];
+            ldsm4(unit_addr<C::CH>(sq + (k / PER) * C::QCHUNKB, mt * 16 + (mat & 1) * 8 + r8,
+                                   (k % PER) * 2 + (mat >> 1)), qa);
+            mma16816(s[mt][0], qa, kb[0], kb[1]);
+            mma16816(s[mt][1], qa, kb[2], kb[3]);
           }
         }
-        float e[2][4];
+        // online softmax; positions outside (pos - window, pos] are masked by selection
+        const int kp = m.key0 + kw + t4 * 2;                // + 8 n + j
+        uint32_t p[MT][4];
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-          const float off = mx[mt][row] == -INFINITY ? 0.f : mx[mt][row];
+        for (int mt = 0; mt < MT; ++mt) {
+          float big[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              e[n][row * 2 + j] = ex2_approx(s[mt][n][row * 2 + j] - off);
-              sum[mt][row] += e[n][row * 2 + j];
+            for (int x = 0; x < 4; ++x) {
+              const int row = x >> 1, key = kp + 8 * n + (x & 1);
+              const bool see = key <= pos[mt][row] && (int64_t)key > (int64_t)pos[mt][row] - a.window &&
+                               key >= 0;
+              s[mt][n][x] = see ? s[mt][n][x] * a.scale_log2 : -INFINITY;
+              big[row] = fmaxf(big[row], s[mt][n][x]);
             }
+#pragma unroll
+          for (int row = 0; row < 2; ++row) {
+            big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 1));
+            big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 2));
+          }
+          // the running max moves only when it grew by more than 2^8 (softmax does
+          // not depend on the offset, and 2^8 is far from overflow)
+          const bool move = big[0] > mx[mt][0] + 8.f || big[1] > mx[mt][1] + 8.f;
+          if (__any_sync(0xffffffffu, move)) {
+            float f[2];
+#pragma unroll
+            for (int row = 0; row < 2; ++row) {
+              const float to = fmaxf(mx[mt][row], big[row]);
+              f[row] = to == -INFINITY ? 1.f : ex2_approx(mx[mt][row] - to);
+              mx[mt][row] = to;
+              sum[mt][row] *= f[row];
+            }
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n) {
+              o[mt][n][0] *= f[0];
+              o[mt][n][1] *= f[0];
+              o[mt][n][2] *= f[1];
+              o[mt][n][3] *= f[1];
+            }
+          }
+          float e[2][4];
+#pragma unroll
+          for (int row = 0; row < 2; ++row) {
+            const float off = mx[mt][row] == -INFINITY ? 0.f : mx[mt][row];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                e[n][row * 2 + j] = ex2_approx(s[mt][n][row * 2 + j] - off);
+                sum[mt][row] += e[n][row * 2 + j];
+              }
+          }
+          p[mt][0] = pack_bf16x2(e[0][0], e[0][1]);
+          p[mt][1] = pack_bf16x2(e[0][2], e[0][3]);
+          p[mt][2] = pack_bf16x2(e[1][0], e[1][1]);
+          p[mt][3] = pack_bf16x2(e[1][2], e[1][3]);
         }
-        p[mt][0] = pack_bf16x2(e[0][0], e[0][1]);
-        p[mt][1] = pack_bf16x2(e[0][2], e[0][3]);
-        p[mt][2] = pack_bf16x2(e[1][0], e[1][1]);
-        p[mt][3] = pack_bf16x2(e[1][2], e[1][3]);
+        // O += P V
+        if (!have_v) {
+          ok = wait(C::B_KVFULL + slot, phase);
+          if (!ok) break;
+          have_v = true;
+        }
+        // V rows that no row of the tile sees may hold anything (NaN): they enter as zeros
+        const bool edge = m.key0 + kw < m.lo || m.key0 + kw + 16 > m.hi;
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+        if (edge)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k0 = kp + 8 * h;
+            keep[h] = (k0 >= m.lo && k0 < m.hi ? 0x0000ffffu : 0u) |
+                      (k0 + 1 >= m.lo && k0 + 1 < m.hi ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+        for (int n = 0; n < DH / 16; ++n) {
+          constexpr int PER = C::CH / 16;
+          uint32_t vb[4];
+          ldsm4t(unit_addr<C::CH>(sv + (n / PER) * C::CHUNKB, kw + (mat & 1) * 8 + r8,
+                                  (n % PER) * 2 + (mat >> 1)), vb);
+          if (edge) {
+            vb[0] &= keep[0];
+            vb[1] &= keep[1];
+            vb[2] &= keep[0];
+            vb[3] &= keep[1];
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(o[mt][2 * n], p[mt], vb[0], vb[1]);
+            mma16816(o[mt][2 * n + 1], p[mt], vb[2], vb[3]);
+          }
+        }
       }
-      // O += P V
-      ok = mbar_wait(bar(C::B_KVFULL + slot), phase, abort_flag, kChunkTimeoutNs);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const uint32_t sv = base + C::OFF_KV + slot * C::SLOTB;
-      // V rows that no row of the tile sees may hold anything (NaN): they enter as zeros
-      const bool edge = m.key0 < m.lo || m.key0 + kBN > m.hi;
-      uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-      if (edge)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int k0 = kp + 8 * h;
-          keep[h] = (k0 >= m.lo && k0 < m.hi ? 0x0000ffffu : 0u) |
-                    (k0 + 1 >= m.lo && k0 + 1 < m.hi ? 0xffff0000u : 0u);
-        }
-#pragma unroll
-      for (int n = 0; n < DH / 16; ++n) {
-        constexpr int PER = C::CH / 16;
-        uint32_t vb[4];
-        ldsm4t(unit_addr<C::CH>(sv + (n / PER) * C::CHUNKB, kw + (mat & 1) * 8 + r8,
-                                (n % PER) * 2 + (mat >> 1)), vb);
-        if (edge) {
-          vb[0] &= keep[0];
-          vb[1] &= keep[1];
-          vb[2] &= keep[0];
-          vb[3] &= keep[1];
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          mma16816(o[mt][2 * n], p[mt], vb[0], vb[1]);
-          mma16816(o[mt][2 * n + 1], p[mt], vb[2], vb[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_KVEMPTY + slot));
+      // (a slot is given back only once its copy has landed, read or not)
+      if (ok && !have_v) ok = wait(C::B_KVFULL + slot, phase);
+      if (!ok) break;
+      arrive(C::B_KVEMPTY + kslot);
+      arrive(C::B_KVEMPTY + slot);
       if (++slot == (uint32_t)C::NS) {
         slot = 0;
         phase ^= 1u;
       }
       if (!(m.flags & kLast)) continue;
+      arrive(C::B_QEMPTY + qn % C::QST);
+      ++qn;
 
       // ------------------------------------------- the item (or piece) is done
+      if (merges > 0 && !wait(C::B_FREE, (merges - 1) & 1u)) break;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int row = 0; row < 2; ++row) {
           sum[mt][row] += __shfl_xor_sync(0xffffffffu, sum[mt][row], 1);
           sum[mt][row] += __shfl_xor_sync(0xffffffffu, sum[mt][row], 2);
-          if (t4 == 0)
-            mls[warp * C::R + mt * 16 + row * 8 + g8] = make_float2(mx[mt][row], sum[mt][row]);
+          const int r = warp * C::R + mt * 16 + row * 8 + g8;
+          if (t4 == 0) mls[r] = make_float2(mx[mt][row], sum[mt][row]);
+#pragma unroll
+          for (int n = 0; n < DH / 8; ++n)
+            *reinterpret_cast<float2*>(mrg + r * (DH + 4) + n * 8 + t4 * 2) =
+                make_float2(o[mt][n][2 * row], o[mt][n][2 * row + 1]);
         }
-      if (!meet()) break;
-      float all[MT][2], tot[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int row = 0; row < 2; ++row) {
-          const int r = mt * 16 + row * 8 + g8;
-          float top = -INFINITY, l = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, mls[w * C::R + r].x);
-          const float off = top == -INFINITY ? 0.f : top;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 v = mls[w * C::R + r];
-            l = fmaf(v.y, ex2_approx(v.x - off), l);
-          }
-          all[mt][row] = top;
-          tot[mt][row] = l;
-          const float f = ex2_approx(mx[mt][row] - off);
-#pragma unroll
-          for (int n = 0; n < DH / 8; ++n) {
-            o[mt][n][2 * row] *= f;
-            o[mt][n][2 * row + 1] *= f;
-          }
-        }
-      // O of warps 2, 3 goes to warps 0, 1, then warp 1's to warp 0
-      auto place = [&](int who, int r, int n) {
-        return mrg + ((int64_t)who * C::R + r) * (DH + 4) + n * 8 + t4 * 2;
-      };
-#pragma unroll
-      for (int step = 2; step > 0; step >>= 1) {
-        if (warp >= step && warp < 2 * step)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < DH / 8; ++n)
-#pragma unroll
-              for (int row = 0; row < 2; ++row)
-                *reinterpret_cast<float2*>(place(warp - step, mt * 16 + row * 8 + g8, n)) =
-                    make_float2(o[mt][n][2 * row], o[mt][n][2 * row + 1]);
-        ok = ok && meet();
-        if (warp < step)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < DH / 8; ++n)
-#pragma unroll
-              for (int row = 0; row < 2; ++row) {
-                const float2 v = *reinterpret_cast<const float2*>(place(warp, mt * 16 + row * 8 + g8, n));
-                o[mt][n][2 * row] += v.x;
-                o[mt][n][2 * row + 1] += v.y;
-              }
-        ok = ok && meet();
+      arrive(C::B_JOIN);
+      if (!wait(C::B_JOIN, merges & 1u)) break;
+      const int kvh = m.vhead / a.vheads, part = m.vhead - kvh * a.vheads;
+      const int head0 = kvh * a.group + part * a.vgroup;
+      const int nh = min(a.vgroup, a.group - part * a.vgroup);
+      const bool whole = (m.flags & kBegins) && (m.flags & kEnds);
+      // a piece that holds the item's first block is the part's last, else its first
+      const int64_t at = 2 * worker + ((m.flags & kBegins) ? 1 : 0);
+      if (!whole && threadIdx.x == 0) {
+        ChunkPiece pc = {};
+        pc.token0 = m.token0;
+        pc.tokens = m.tokens;
+        pc.head0 = head0;
+        pc.heads = nh;
+        pc.ends = (m.flags & kEnds) ? 1 : 0;
+        a.piece[at] = pc;
       }
-      if (!ok) break;
-      if (warp == 0) {
-        const int kvh = m.vhead / a.vheads, part = m.vhead - kvh * a.vheads;
-        const int head0 = kvh * a.group + part * a.vgroup;
-        const int nh = min(a.vgroup, a.group - part * a.vgroup);
-        const bool whole = (m.flags & kBegins) && (m.flags & kEnds);
-        // a piece that holds the item's first block is the part's last, else its first
-        const int64_t at = 2 * worker + ((m.flags & kBegins) ? 1 : 0);
-        if (!whole && lane == 0) {
-          ChunkPiece pc = {};
-          pc.token0 = m.token0;
-          pc.tokens = m.tokens;
-          pc.head0 = head0;
-          pc.heads = nh;
-          pc.ends = (m.flags & kEnds) ? 1 : 0;
-          a.piece[at] = pc;
+      // four columns of a row to a thread: along the rows of O, or along the workspace's row groups
+#pragma unroll 1
+      for (int e = threadIdx.x; e < C::R * DH / 4; e += kWarps * 32) {
+        const int r = whole ? e / (DH / 4) : e % C::R, c4 = whole ? e % (DH / 4) : e / C::R;
+        const int tk = r / a.vgroup, h = r - tk * a.vgroup;
+        if (tk >= m.tokens || h >= nh) continue;
+        float2 ml[kWarps];
+        float top = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          ml[w] = mls[w * C::R + r];
+          top = fmaxf(top, ml[w].x);
         }
+        const float off = top == -INFINITY ? 0.f : top;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int row = 0; row < 2; ++row) {
-            const int r = mt * 16 + row * 8 + g8, tk = r / a.vgroup, h = r - tk * a.vgroup;
-            if (tk >= m.tokens || h >= nh) continue;
-            const float l = tot[mt][row], top = all[mt][row];
-            if (whole) {
-              const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-              const int64_t t = m.token0 + tk;
-              __nv_bfloat16* dst = a.o + (t * a.hq + head0 + h) * DH + t4 * 2;
-#pragma unroll
-              for (int n = 0; n < DH / 8; ++n)
-                *reinterpret_cast<uint32_t*>(dst + n * 8) =
-                    pack_bf16x2(o[mt][n][2 * row] * inv, o[mt][n][2 * row + 1] * inv);
-              if (a.lse && t4 == 0)
-                a.lse[(int64_t)(head0 + h) * a.T + t] =
-                    l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-            } else {
-              float* dst = a.po + at * a.rows * DH + ((t4 >> 1) * a.rows + r) * 4 + (t4 & 1) * 2;
-#pragma unroll
-              for (int n = 0; n < DH / 8; ++n)
-                *reinterpret_cast<float2*>(dst + n * 8 * a.rows) =
-                    make_float2(o[mt][n][2 * row], o[mt][n][2 * row + 1]);
-              if (t4 == 0) a.ml[at * a.rows + r] = make_float2(top, l);
-            }
-          }
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2_approx(ml[w].x - off);
+          const float4 x = *reinterpret_cast<const float4*>(mrg + (w * C::R + r) * (DH + 4) + c4 * 4);
+          l = fmaf(ml[w].y, f, l);
+          v.x = fmaf(x.x, f, v.x);
+          v.y = fmaf(x.y, f, v.y);
+          v.z = fmaf(x.z, f, v.z);
+          v.w = fmaf(x.w, f, v.w);
+        }
+        if (whole) {
+          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+          const int64_t t = m.token0 + tk;
+          *reinterpret_cast<uint2*>(a.o + (t * a.hq + head0 + h) * DH + c4 * 4) =
+              make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+          if (a.lse && c4 == 0)
+            a.lse[(int64_t)(head0 + h) * a.T + t] =
+                l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float4*>(a.po + at * a.rows * DH + ((int64_t)c4 * a.rows + r) * 4) = v;
+          if (c4 == 0) a.ml[at * a.rows + r] = make_float2(top, l);
+        }
       }
+      arrive(C::B_FREE);
+      ++merges;
     }
   }
   __syncthreads();
@@ -640,7 +608,7 @@ cudaError_t launch_rows(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t 
   using C = Cfg<DH, MT>;
   CUtensorMap mq, mk, mv;
   const CUtensorMapSwizzle sw = DH < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  if (!chunk_maps(a, c, DH, C::CH, kBN, sw, &mq, &mk, &mv)) return cudaErrorInvalidValue;
+  if (!chunk_maps(a, c, DH, C::CH, C::kBN, sw, &mq, &mk, &mv)) return cudaErrorInvalidValue;
   auto kern = chunk_rows_kernel<DH, MT>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(kern, (int)C::SMEM, done);
@@ -660,9 +628,11 @@ ChunkLayout chunk_layout(const gdpa_cache_t& c, int hq, int max_n) {
   ChunkLayout L;
   const int group = hq / c.hk;
   // one row tile of 16, or of 32, where it holds all of a sample's rows; pairs of 128-row
-  // tiles on the tensor core's tcgen05 path beyond that
+  // tiles on the tensor core's tcgen05 path beyond that.  At dh = 128 a thread has no registers for 32 rows of O
+  // beside the rest: 32 rows over 8 x 15 k positions, 8 kv heads, took 199 us in one tile of 32 and 100 us on the
+  // tcgen05 path (dh = 64: 75 and 83 us).
   const int64_t need = (int64_t)group * max_n;
-  L.tiles = need > 32;
+  L.tiles = need > (c.dh == 128 ? 16 : 32);
   L.mt = need <= 16 ? 1 : 2;
   L.tile_rows = L.tiles ? 128 : 16 * L.mt;
   L.rows = L.tiles ? 256 : L.tile_rows;
@@ -791,7 +761,7 @@ extern "C" gdpa_status_t gdpa_chunk_fwd(const gdpa_cache_t* cache, int32_t B, in
   a.rt1 = L.rt1;
   a.rows = L.rows;
   a.tile_rows = L.tile_rows;
-  a.bn_shift = L.tiles ? 7 : kBNShift;
+  a.bn_shift = L.tiles ? 7 : chunk_rows_shift(cache->dh);
   a.num_pages = cache->num_pages;
   a.max_pages = cache->max_pages;
   a.page_shift = log2_int(cache->page);
@@ -800,8 +770,10 @@ extern "C" gdpa_status_t gdpa_chunk_fwd(const gdpa_cache_t* cache, int32_t B, in
   cudaError_t e;
 #define GDPA_ROWS(DH) \
   (L.mt == 1 ? launch_rows<DH, 1>(a, *cache, st) : launch_rows<DH, 2>(a, *cache, st))
-  e = L.tiles ? launch_chunk_tiles(a, *cache, st)
-              : cache->dh == 32 ? GDPA_ROWS(32) : cache->dh == 64 ? GDPA_ROWS(64) : GDPA_ROWS(128);
+  e = L.tiles            ? launch_chunk_tiles(a, *cache, st)
+      : cache->dh == 32 ? GDPA_ROWS(32)
+      : cache->dh == 64 ? GDPA_ROWS(64)
+                        : launch_rows<128, 1>(a, *cache, st);
 #undef GDPA_ROWS
   if (e == cudaSuccess) e = launch_chunk_join(a, cache->dh, (WsHeader*)workspace, st);
   return finish(e);

@@ -14,6 +14,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 constexpr uint64_t kChunkTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy wait is microseconds
 
+// log2 of the positions of a block of the kernel for few rows: 64 at dh = 128, 256 at dh = 32 (16 KB of K)
+constexpr int chunk_rows_shift(int dh) { return dh == 128 ? 6 : dh == 64 ? 7 : 8; }
+
 // A piece of an item whose blocks are shared with other workers (or none:
 // tokens = 0).  Its rows' (max in log2 units, sum) and unnormalised O are at the
 // same index of the workspace's ml and po arrays.

@@ -87,7 +87,7 @@ def _blocks(n, ctx, window, rt, bn, tile):
 @pytest.mark.parametrize("seed", range(60))
 def test_cut_matches_enumeration(host, seed):
     r = random.Random(seed)
-    n, rt, shift = r.randint(1, 900), r.choice([1, 2, 3, 5, 16, 21, 32, 42, 64, 128]), r.choice([6, 7])
+    n, rt, shift = r.randint(1, 900), r.choice([1, 2, 3, 5, 16, 21, 32, 42, 64, 128]), r.choice([6, 7, 8])
     ctx = r.choice([0, r.randint(0, 3000), -r.randint(1, 2 * n), -n])
     window = r.choice([1, r.randint(1, 500), 2**31 - 1])
     tiles = -(-n // rt)
