@@ -24,12 +24,12 @@ using namespace sm100;
 // fp32 (4 vectors: 467 us at 2048 wide instead of 447, 8 in 8 warps: 635); backward y, dn, f, G, the gate and up
 // to three sums, for which 16 warps have too few registers and 8 hide too little (1024 wide, shared
 // gates: 496 and 458 us where 12 warps took 360).
-constexpr int kWarpsFwd = 16, kWarpsBwd = 12, kMaxFwd = 2, kMaxBwd = 2;
+constexpr int kWarpsFwd = 16, kWarpsBwd = 12, kWarpsWide = 16, kMaxFwd = 2, kMaxBwd = 2;
 constexpr uint64_t kNormTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy wait is microseconds
 // Rows in flight of a warp, the current one among them.  Two are enough, and what a longer ring takes is missing
 // in L1, which holds the weights: backward, 1024 wide, 4 rows 360 us, 2 rows 326 us.
 constexpr int kStages = 2;
-constexpr uint32_t kRingBytes = 200 * 1024;          // of a block, at most; up to 24 KB of sums come behind it
+constexpr uint32_t kRingBytes = 192 * 1024;          // of a block, at most; up to 32 KB of sums come behind it
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -377,8 +377,10 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
 }
 
 // (A gate of GDPA_GATE_SAMPLE is one row per sample, whose gradient accumulates over the sample's rows.)
-template <typename E, int NV, bool AL, bool BLOCK, bool PRE, bool POST, int GATE>
-__global__ void __launch_bounds__(kWarpsBwd * 32, 1)
+// WARPS: kWarpsBwd, or kWarpsWide for rows that more warps have to share: 128 registers spill some of the row,
+// still far from the registers' form (14 k bf16 rows of 8192 624 us, there 1187).
+template <typename E, int NV, int WARPS, bool AL, bool BLOCK, bool PRE, bool POST, int GATE>
+__global__ void __launch_bounds__(WARPS * 32, 1)
 norm_stream_bwd_kernel(const NormArgs a, int W) {
   pdl_trigger();
   constexpr bool SHARED = GATE == GDPA_GATE_SAMPLE;
@@ -642,37 +644,41 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
 
 using Kernel = void (*)(const NormArgs, int);
 
-template <typename E, int NV, bool AL, bool BACKWARD, bool PRE, bool POST, int GATE>
+// WARPS = 0: forward
+template <typename E, int NV, int WARPS, bool AL, bool PRE, bool POST, int GATE>
 Kernel kernel_of() {
-  if constexpr (BACKWARD)
-    return norm_stream_bwd_kernel<E, NV, AL, true, PRE, POST, GATE>;
+  if constexpr (WARPS > 0)
+    return norm_stream_bwd_kernel<E, NV, WARPS, AL, true, PRE, POST, GATE>;
   else
     return norm_stream_fwd_kernel<E, NV, AL, true, POST, GATE>;
 }
-template <typename E, int NV, bool AL, bool BACKWARD, bool PRE, bool POST>
+template <typename E, int NV, int WARPS, bool AL, bool PRE, bool POST>
 Kernel kernel_of(const NormArgs& a) {
-  if (a.gate_kind == GDPA_GATE_TOKEN) return kernel_of<E, NV, AL, BACKWARD, PRE, POST, GDPA_GATE_TOKEN>();
-  if (a.gate_kind == GDPA_GATE_SAMPLE) return kernel_of<E, NV, AL, BACKWARD, PRE, POST, GDPA_GATE_SAMPLE>();
-  return kernel_of<E, NV, AL, BACKWARD, PRE, POST, GDPA_GATE_NONE>();
+  if (a.gate_kind == GDPA_GATE_TOKEN) return kernel_of<E, NV, WARPS, AL, PRE, POST, GDPA_GATE_TOKEN>();
+  if (a.gate_kind == GDPA_GATE_SAMPLE) return kernel_of<E, NV, WARPS, AL, PRE, POST, GDPA_GATE_SAMPLE>();
+  return kernel_of<E, NV, WARPS, AL, PRE, POST, GDPA_GATE_NONE>();
 }
-template <typename E, int NV, bool AL, bool BACKWARD>
+template <typename E, int NV, int WARPS, bool AL>
 Kernel kernel_of(const NormArgs& a) {
   if (!a.f) {
-    if constexpr (BACKWARD)
-      return norm_stream_bwd_kernel<E, NV, AL, false, true, false, GDPA_GATE_NONE>;
+    if constexpr (WARPS > 0)
+      return norm_stream_bwd_kernel<E, NV, WARPS, AL, false, true, false, GDPA_GATE_NONE>;
     else
       return norm_stream_fwd_kernel<E, NV, AL, false, false, GDPA_GATE_NONE>;
   }
-  if constexpr (BACKWARD)             // (forward, n is a test beside the row's sum)
+  if constexpr (WARPS > 0)            // (forward, n is a test beside the row's sum)
     if (!a.w_pre)
-      return a.w_post ? kernel_of<E, NV, AL, BACKWARD, false, true>(a) : kernel_of<E, NV, AL, BACKWARD, false, false>(a);
-  return a.w_post ? kernel_of<E, NV, AL, BACKWARD, true, true>(a) : kernel_of<E, NV, AL, BACKWARD, true, false>(a);
+      return a.w_post ? kernel_of<E, NV, WARPS, AL, false, true>(a)
+                      : kernel_of<E, NV, WARPS, AL, false, false>(a);
+  return a.w_post ? kernel_of<E, NV, WARPS, AL, true, true>(a) : kernel_of<E, NV, WARPS, AL, true, false>(a);
 }
 
 template <typename E, bool AL>
-Kernel dispatch(const NormArgs& a, int nv, bool backward) {
-  if (backward) return nv == kMaxBwd ? kernel_of<E, kMaxBwd, AL, true>(a) : kernel_of<E, kMaxBwd / 2, AL, true>(a);
-  return nv == kMaxFwd ? kernel_of<E, kMaxFwd, AL, false>(a) : kernel_of<E, kMaxFwd / 2, AL, false>(a);
+Kernel dispatch(const NormArgs& a, const StreamPlan& p, bool backward) {
+  if (!backward)
+    return p.nv == kMaxFwd ? kernel_of<E, kMaxFwd, 0, AL>(a) : kernel_of<E, kMaxFwd / 2, 0, AL>(a);
+  if (p.warps > kWarpsBwd) return kernel_of<E, kMaxBwd, kWarpsWide, AL>(a);
+  return p.nv == kMaxBwd ? kernel_of<E, kMaxBwd, kWarpsBwd, AL>(a) : kernel_of<E, kMaxBwd / 2, kWarpsBwd, AL>(a);
 }
 
 }  // namespace
@@ -691,7 +697,8 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   int nv = most / 2;
   while (nv < most && nv * 32 * vec < d) nv *= 2;
   const int w = (d + nv * 32 * vec - 1) / (nv * 32 * vec);
-  const int warps = (backward ? kWarpsBwd : kWarpsFwd) / w * w;
+  const int most_warps = !backward ? kWarpsFwd : w <= kWarpsBwd ? kWarpsBwd : kWarpsWide;
+  const int warps = most_warps / w * w;
   if (warps == 0) return p;
   int64_t groups = (int64_t)device_sm_count() * (warps / w);
   if (groups > T) groups = T;
@@ -711,10 +718,10 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
 cudaError_t launch_norm_stream(const NormArgs& a, const StreamPlan& p, int dtype, bool backward,
                                cudaStream_t st) {
   const bool bf16 = dtype == GDPA_DTYPE_BF16, aligned = a.d % (bf16 ? 8 : 4) == 0;
-  Kernel kern = bf16 ? aligned ? dispatch<__nv_bfloat16, true>(a, p.nv, backward)
-                               : dispatch<__nv_bfloat16, false>(a, p.nv, backward)
-                     : aligned ? dispatch<float, true>(a, p.nv, backward)
-                               : dispatch<float, false>(a, p.nv, backward);
+  Kernel kern = bf16 ? aligned ? dispatch<__nv_bfloat16, true>(a, p, backward)
+                               : dispatch<__nv_bfloat16, false>(a, p, backward)
+                     : aligned ? dispatch<float, true>(a, p, backward)
+                               : dispatch<float, false>(a, p, backward);
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   if (e != cudaSuccess) return e;
