@@ -336,7 +336,9 @@ def test_bad_offsets_lengths_and_pages_are_reported(max_n):
 
 def test_same_bits_again_and_beside_another_call():
     """Two calls on two streams with workspaces of their own give the bits of a call alone."""
-    for n, kv, dh in (([1] * 20, list(range(50, 1050, 50)), 128), ([300, 20], [2000, 500], 64)):
+    for n, kv, dh in (([1] * 20, list(range(50, 1050, 50)), 128), ([300, 20], [2000, 500], 64),
+                      ([130, 0, 7, 301, 64], [900, 5, 7, 1000, 3000], 32),
+                      ([33, 700, 1, 90], [500, 700, 2000, 91], 128)):
         off, offd, table, ck, cv, q, scale = _chunk_case(n, kv, 8, 2, dh, 16, 13)
         args = (q.to(DEV), offd, _int32(kv), _int32(table), ck.to(DEV), cv.to(DEV), scale)
         want, wl = G.chunk_fwd(*args, max_n=max(n))
@@ -348,6 +350,68 @@ def test_same_bits_again_and_beside_another_call():
         torch.cuda.synchronize()
         for o, lse in outs:
             assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("n", [[1, 1, 1], [40, 3, 100]])
+def test_shared_pages_and_no_lse(n):
+    """Samples that begin with the same pages (a common prefix), and a call that asks for no LSE."""
+    kv = [200, 150, 130]
+    off, offd, table, ck, cv, q, scale = _chunk_case(n, kv, 4, 2, 64, 16, 17)
+    table[1, :4], table[2, :4] = table[0, :4], table[0, :4]
+    args = (q.to(DEV), offd, _int32(kv), _int32(table), ck.to(DEV), cv.to(DEV), scale)
+    o, lse = G.chunk_fwd(*args, max_n=max(n), want_lse=False)
+    assert lse is None
+    want, _, mag, size = ref.chunk(_np(q), off, kv, table, ck.float().numpy(), cv.float().numpy(), scale)
+    delta = 68 * 2.0 ** -24 * size + 2.0 ** -21
+    _near(o, want, 1.001 * (2.0 ** -8 * (mag + np.abs(want)) + 2 * delta.T[:, :, None] * mag))
+
+
+def test_cache_offsets_past_32_bits():
+    """Pages whose elements lie beyond 2^31 in the cache: written by the append, read by both attention
+    kernels; and rows beyond 2^31 elements in a strided rotation."""
+    hk, page, dh, P = 8, 128, 128, 16500
+    ck, cv = (torch.empty(P, hk, page, dh, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    assert ck.numel() > 2 ** 31
+    g = torch.Generator(device=DEV).manual_seed(18)
+    for n in (200, 1):
+        table = _int32([[P - 1, P - 3]])
+        k, v, q = (torch.randn(m, h, dh, generator=g, device=DEV).bfloat16()
+                   for m, h in ((200, hk), (200, hk), (n, hk)))
+        G.cache_append(k, v, _int32([0, 200]), _int32([200]), table, ck, cv)
+        o, _ = G.chunk_fwd(q, _int32([0, n]), _int32([200]), table, ck, cv, 0.1, max_n=n)
+        want, _, mag, size = ref.chunk(_np(q), [0, n], [200], np.array([[1, 0]]),
+                                       *(torch.cat([torch.nn.functional.pad(x[128:], (0, 0, 0, 0, 0, 56)),
+                                                    x[:128]]).view(2, page, hk, dh).transpose(1, 2)
+                                         .float().cpu().numpy() for x in (k, v)), 0.1)
+        delta = 132 * 2.0 ** -24 * size + 2.0 ** -21
+        _near(o, want, 1.001 * (2.0 ** -8 * (mag + np.abs(want)) + 2 * delta.T[:, :, None] * mag))
+    del cv
+    rows = ck.view(P, hk * page * dh)
+    assert (P - 1) * rows.stride(0) > 2 ** 31
+    rows[-1, :256] = torch.randn(256, generator=g, device=DEV).bfloat16()
+    x = rows[:, :256].unflatten(1, (2, 128))
+    y = G.rotary(G.rotary_spec(128), x, positions=torch.arange(P, dtype=torch.int32, device=DEV))
+    want, mag = ref.rotary(_np(x[-1:]), np.array([P - 1]), rot=128)
+    _near(y[-1:], want, HALF[torch.bfloat16] * np.abs(want) + 8 * 2.0 ** -24 * mag)
+
+
+def test_calls_on_another_stream():
+    """`stream` as a torch stream and as a raw handle: the call and what it allocates belong to that stream."""
+    off, offd, table, ck, cv, q, scale = _chunk_case([2, 3], [40, 50], 4, 2, 64, 16, 19)
+    args = (q.to(DEV), offd, _int32([40, 50]), _int32(table), ck.to(DEV), cv.to(DEV), scale)
+    x, w = torch.randn(30, 96, device=DEV), torch.ones(96, device=DEV)
+    want, wl = G.chunk_fwd(*args, max_n=3)
+    _, wn = G.block_norm_fwd(x, w_pre=w)
+    wr = G.rotary(G.rotary_spec(64), args[0], offsets=offd)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for st in (s, s.cuda_stream):
+        o, lse = G.chunk_fwd(*args, max_n=3, stream=st)
+        _, n = G.block_norm_fwd(x, w_pre=w, stream=st)
+        r = G.rotary(G.rotary_spec(64), args[0], offsets=offd, stream=st)
+        s.synchronize()
+        assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(n, wn) and torch.equal(r, wr)
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
 
 
 def test_empty_batch():
