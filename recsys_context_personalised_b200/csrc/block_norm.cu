@@ -9,6 +9,9 @@
 //   df = r_f (w_post du - fh mean(w_post du fh)),    fh = f r_f
 //   dw_pre = sum_t dn yh,  dw_post = sum_t du fh
 //
+// This file has the entry points and the form that keeps rows in registers, for many narrow rows and very
+// wide fp32 ones; block_norm_stream.cu has the form for all others.
+//
 // Bound: memory, every row once.  A row is spread over TPR threads that keep
 // it in registers (NV vectors of VEC elements each) between its two
 // reductions.  A group of TPR threads walks a contiguous range of rows, with the
@@ -465,14 +468,13 @@ template <typename E, int V16>
 cudaError_t dispatch(const NormArgs& a, const Plan& p, bool backward, cudaStream_t st) {
 #define GDPA_NORM(VEC, NV) \
   return backward ? launch_bwd<E, VEC, NV>(a, p, st) : launch_fwd<E, VEC, NV>(a, p, st)
-  if (p.vec == 1) {
-    if (p.nv == 4) GDPA_NORM(1, 4);
-    if (p.nv == 8) GDPA_NORM(1, 8);
-    GDPA_NORM(1, 16);
+  // (what stream_plan leaves: rows narrower than 128, and fp32 rows beyond 4,096)
+  if (p.vec == 1 && p.nv == 4) GDPA_NORM(1, 4);
+  if (p.vec > 1 && p.nv == 1) GDPA_NORM(V16, 1);
+  if constexpr (V16 == 4) {
+    if (p.vec == 1) GDPA_NORM(1, 16);
+    GDPA_NORM(4, 4);
   }
-  if (p.nv == 1) GDPA_NORM(V16, 1);
-  if (p.nv == 2) GDPA_NORM(V16, 2);
-  if constexpr (V16 == 4) GDPA_NORM(4, 4);
   return cudaErrorInvalidValue;
 #undef GDPA_NORM
 }
