@@ -642,15 +642,23 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
   }
 }
 
-using Kernel = void (*)(const NormArgs, int);
+struct Kernel {
+  void (*fn)(const NormArgs, int);
+  std::atomic<uint64_t>* allowed;     // devices that have its shared memory allowed
+};
+template <void (*FN)(const NormArgs, int)>
+Kernel entry() {
+  static std::atomic<uint64_t> allowed{0};
+  return {FN, &allowed};
+}
 
 // WARPS = 0: forward
 template <typename E, int NV, int WARPS, bool AL, bool PRE, bool POST, int GATE>
 Kernel kernel_of() {
   if constexpr (WARPS > 0)
-    return norm_stream_bwd_kernel<E, NV, WARPS, AL, true, PRE, POST, GATE>;
+    return entry<norm_stream_bwd_kernel<E, NV, WARPS, AL, true, PRE, POST, GATE>>();
   else
-    return norm_stream_fwd_kernel<E, NV, AL, true, POST, GATE>;
+    return entry<norm_stream_fwd_kernel<E, NV, AL, true, POST, GATE>>();
 }
 template <typename E, int NV, int WARPS, bool AL, bool PRE, bool POST>
 Kernel kernel_of(const NormArgs& a) {
@@ -662,9 +670,9 @@ template <typename E, int NV, int WARPS, bool AL>
 Kernel kernel_of(const NormArgs& a) {
   if (!a.f) {
     if constexpr (WARPS > 0)
-      return norm_stream_bwd_kernel<E, NV, WARPS, AL, false, true, false, GDPA_GATE_NONE>;
+      return entry<norm_stream_bwd_kernel<E, NV, WARPS, AL, false, true, false, GDPA_GATE_NONE>>();
     else
-      return norm_stream_fwd_kernel<E, NV, AL, false, false, GDPA_GATE_NONE>;
+      return entry<norm_stream_fwd_kernel<E, NV, AL, false, false, GDPA_GATE_NONE>>();
   }
   if constexpr (WARPS > 0)            // (forward, n is a test beside the row's sum)
     if (!a.w_pre)
@@ -718,15 +726,14 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
 cudaError_t launch_norm_stream(const NormArgs& a, const StreamPlan& p, int dtype, bool backward,
                                cudaStream_t st) {
   const bool bf16 = dtype == GDPA_DTYPE_BF16, aligned = a.d % (bf16 ? 8 : 4) == 0;
-  Kernel kern = bf16 ? aligned ? dispatch<__nv_bfloat16, true>(a, p, backward)
+  const Kernel kern = bf16 ? aligned ? dispatch<__nv_bfloat16, true>(a, p, backward)
                                : dispatch<__nv_bfloat16, false>(a, p, backward)
                      : aligned ? dispatch<float, true>(a, p, backward)
                                : dispatch<float, false>(a, p, backward);
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  const cudaError_t e = allow_smem(kern.fn, (int)kRingBytes + 32 * 1024, *kern.allowed);
   if (e != cudaSuccess) return e;
   KernelScope ks_(backward ? "gdpa_block_norm_bwd" : "gdpa_block_norm_fwd", st);
-  kern<<<p.blocks, p.warps * 32, p.smem, st>>>(a, p.warps_row);
+  kern.fn<<<p.blocks, p.warps * 32, p.smem, st>>>(a, p.warps_row);
   return cudaGetLastError();
 }
 

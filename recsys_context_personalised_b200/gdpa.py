@@ -423,22 +423,21 @@ def _need(ok, where: str, what: str) -> None:
         raise GdpaError(1, f"{where} ({what})")
 
 
-def _operand(where, name, t, dtype, shape, device) -> None:
-    """A contiguous tensor of that type and shape on `device`."""
+def _operand(where, name, t, dtype, shape, dev) -> int:
+    """Address of a contiguous tensor of that type and shape on device number `dev`."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_contiguous()):
-        raise GdpaError(1, f"{where} ({name}: a contiguous {dtype} tensor {list(shape)} on {device})")
+            and t.get_device() == dev and t.is_contiguous()):
+        raise GdpaError(1, f"{where} ({name}: a contiguous {dtype} tensor {list(shape)} on cuda:{dev})")
+    return t.data_ptr()
 
 
-def _heads(where, name, t, dtype, shape, device) -> int:
+def _heads(where, name, t, dtype, shape, dev) -> int:
     """A [T, h, dh] tensor whose heads are contiguous; returns its token stride."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device):
-        raise GdpaError(1, f"{where} ({name}: {dtype} {list(shape)} on {device}, heads contiguous)")
-    row, head, one = t.stride()
-    if one != 1 or (head != shape[2] and shape[1] != 1):
-        raise GdpaError(1, f"{where} ({name}: {dtype} {list(shape)} on {device}, heads contiguous)")
-    return row if shape[0] > 1 else shape[1] * shape[2]
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        row, head, one = t.stride()
+        if one == 1 and (head == shape[2] or shape[1] == 1):
+            return row if shape[0] > 1 else shape[1] * shape[2]
+    raise GdpaError(1, f"{where} ({name}: {dtype} {list(shape)} on cuda:{dev}, heads contiguous)")
 
 
 # The current device and its current stream without the Python objects around them (of which a
@@ -449,31 +448,32 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 
 class _On:
-    """Makes a tensor's device current, and `stream` (when given) the stream
-    that allocations belong to, for the length of a call; gives the stream's handle."""
-    __slots__ = ("dev", "ctx")
+    """Makes a device current, and `stream` (when given) the stream that allocations
+    belong to, for the length of a call."""
 
-    def __init__(self, where, t, stream):
-        _need(isinstance(t, torch.Tensor) and t.is_cuda, where, "a CUDA tensor")
-        self.dev = t.get_device()
-        self.ctx = ()
-        if stream is None and self.dev == _current_device():
-            return
-        self.ctx = [torch.cuda.device(self.dev)]
+    def __init__(self, dev, stream):
+        self.ctx = [torch.cuda.device(dev)]
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-                stream = torch.cuda.ExternalStream(raw, device=t.device)
+                stream = torch.cuda.ExternalStream(raw, device=dev)
             self.ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return _raw_stream(self.dev)
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
+
+
+def _elsewhere(where, t, stream) -> Optional[_On]:
+    """What a call on `t` and `stream` has to run under; None where it is in force already."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda):
+        raise GdpaError(1, f"{where} (a CUDA tensor)")
+    dev = t.get_device()
+    return None if stream is None and dev == _current_device() else _On(dev, stream)
 
 
 def rotary_spec(rot: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
@@ -495,25 +495,29 @@ def rotary(spec: RotarySpec, x: torch.Tensor, offsets=None, kv_len=None, positio
     ``out`` may be ``x``; rows behind the last sample are left as they were (in a
     new ``out``: not set).  ``inverse`` gives the gradient."""
     w = "gdpa_rotary"
-    with _On(w, x, stream) as st:
-        _need(x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32), w,
-              "x: bf16 or fp32 [T, h, dh]")
-        T, h, dh = x.shape
-        xs = _heads(w, "x", x, x.dtype, (T, h, dh), x.device)
-        B = 0
-        if offsets is not None:
-            B = offsets.numel() - 1
-            _operand(w, "offsets", offsets, torch.int32, (B + 1,), x.device)
-        if kv_len is not None:
-            _operand(w, "kv_len", kv_len, torch.int32, (B,), x.device)
-        if positions is not None:
-            _operand(w, "positions", positions, torch.int32, (T,), x.device)
-        if out is None:
-            out = torch.empty((T, h, dh), dtype=x.dtype, device=x.device)
-        ys = _heads(w, "out", out, x.dtype, (T, h, dh), x.device)
-        rc = load().gdpa_rotary(ctypes.byref(spec), DTYPE_BF16 if x.dtype == torch.bfloat16
-                                else DTYPE_F32, B, h, dh, T, _ptr(offsets), _ptr(kv_len),
-                                _ptr(positions), _ptr(x), xs, _ptr(out), ys, int(bool(inverse)), st)
+    on = _elsewhere(w, x, stream)
+    if on:
+        with on:
+            return rotary(spec, x, offsets, kv_len, positions, out, inverse)
+    dt, dev = x.dtype, x.get_device()
+    _need(x.dim() == 3 and dt in (torch.bfloat16, torch.float32), w, "x: bf16 or fp32 [T, h, dh]")
+    T, h, dh = x.shape
+    xs = _heads(w, "x", x, dt, (T, h, dh), dev)
+    B, off, kv, pos = 0, None, None, None
+    if offsets is not None:
+        B = offsets.numel() - 1
+        off = _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
+    if kv_len is not None:
+        kv = _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
+    if positions is not None:
+        pos = _operand(w, "positions", positions, torch.int32, (T,), dev)
+    if out is None:
+        out, ys = torch.empty((T, h, dh), dtype=dt, device=x.device), h * dh
+    else:
+        ys = _heads(w, "out", out, dt, (T, h, dh), dev)
+    rc = load().gdpa_rotary(ctypes.byref(spec), DTYPE_BF16 if dt is torch.bfloat16 else DTYPE_F32, B,
+                            h, dh, T, off, kv, pos, x.data_ptr(), xs, out.data_ptr(), ys,
+                            int(bool(inverse)), _raw_stream(dev))
     if rc:
         raise GdpaError(rc, w)
     return out
@@ -522,15 +526,14 @@ def rotary(spec: RotarySpec, x: torch.Tensor, offsets=None, kv_len=None, positio
 def _cache(where, cache_k, cache_v, page_table, B) -> Cache:
     _need(isinstance(cache_k, torch.Tensor) and cache_k.dim() == 4, where,
           "cache_k: [num_pages, hk, page, dh]")
-    pages, hk, page, dh = cache_k.shape
-    dev = cache_k.device
-    _operand(where, "cache_k", cache_k, torch.bfloat16, (pages, hk, page, dh), dev)
-    _operand(where, "cache_v", cache_v, torch.bfloat16, (pages, hk, page, dh), dev)
     _need(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, where,
           "page_table: [B, max_pages]")
-    _operand(where, "page_table", page_table, torch.int32, (B, page_table.shape[1]), dev)
-    return Cache(_ptr(cache_k), _ptr(cache_v), _ptr(page_table), pages, page_table.shape[1], page,
-                 hk, dh, 0)
+    shape, dev, width = cache_k.shape, cache_k.get_device(), page_table.shape[1]
+    pages, hk, page, dh = shape
+    return Cache(_operand(where, "cache_k", cache_k, torch.bfloat16, shape, dev),
+                 _operand(where, "cache_v", cache_v, torch.bfloat16, shape, dev),
+                 _operand(where, "page_table", page_table, torch.int32, (B, width), dev),
+                 pages, width, page, hk, dh, 0)
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v,
@@ -541,32 +544,41 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, offsets, kv_len, page_table, 
     ``kv_len`` [B] counts each sample's tokens with the new ones.  With ``q``
     [T, hq, dh] its rotation is returned (``q_out``)."""
     w = "gdpa_cache_append"
-    with _On(w, cache_k, stream) as st:
-        dev = cache_k.device
-        _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
-        B = offsets.numel() - 1
-        c = _cache(w, cache_k, cache_v, page_table, B)
-        _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
-        _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
-        T = k.shape[0]
-        ks = _heads(w, "k", k, torch.bfloat16, (T, c.hk, c.dh), dev)
-        vs = _heads(w, "v", v, torch.bfloat16, (T, c.hk, c.dh), dev)
-        hq, qs = 0, 0
-        if q is not None:
-            hq = q.shape[1]
-            qs = _heads(w, "q", q, torch.bfloat16, (T, hq, c.dh), dev)
-            if q_out is None:
-                q_out = torch.empty((T, hq, c.dh), dtype=q.dtype, device=dev)
-            _operand(w, "q_out", q_out, torch.bfloat16, (T, hq, c.dh), dev)
+    on = _elsewhere(w, cache_k, stream)
+    if on:
+        with on:
+            return cache_append(k, v, offsets, kv_len, page_table, cache_k, cache_v, spec, q, q_out,
+                                status_ws)
+    dev = cache_k.get_device()
+    _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
+    B = offsets.numel() - 1
+    c = _cache(w, cache_k, cache_v, page_table, B)
+    _, hk, _, dh = cache_k.shape
+    off = _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
+    kv = _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
+    _need(isinstance(k, torch.Tensor) and k.dim() == 3, w, "k: [T, hk, dh]")
+    T = k.shape[0]
+    ks = _heads(w, "k", k, torch.bfloat16, (T, hk, dh), dev)
+    vs = _heads(w, "v", v, torch.bfloat16, (T, hk, dh), dev)
+    hq, qs, qp, qo = 0, 0, None, None
+    if q is not None:
+        _need(isinstance(q, torch.Tensor) and q.dim() == 3, w, "q: [T, hq, dh]")
+        hq = q.shape[1]
+        qs, qp = _heads(w, "q", q, torch.bfloat16, (T, hq, dh), dev), q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty((T, hq, dh), dtype=torch.bfloat16, device=cache_k.device)
+            qo = q_out.data_ptr()
         else:
-            _need(q_out is None, w, "q_out without q")
-        if status_ws is not None:
-            _need(status_ws.is_cuda and status_ws.device == dev and status_ws.is_contiguous()
-                  and status_ws.numel() * status_ws.element_size() >= 256, w,
-                  "status_ws: 256 bytes on the device")
-        rc = load().gdpa_cache_append(None if spec is None else ctypes.byref(spec), ctypes.byref(c),
-                                      B, hq, T, _ptr(offsets), _ptr(kv_len), _ptr(q), qs,
-                                      _ptr(q_out), _ptr(k), ks, _ptr(v), vs, _ptr(status_ws), st)
+            qo = _operand(w, "q_out", q_out, torch.bfloat16, (T, hq, dh), dev)
+    else:
+        _need(q_out is None, w, "q_out without q")
+    if status_ws is not None:
+        _need(status_ws.get_device() == dev and status_ws.is_contiguous()
+              and status_ws.numel() * status_ws.element_size() >= 256, w,
+              "status_ws: 256 bytes on the device")
+    rc = load().gdpa_cache_append(None if spec is None else ctypes.byref(spec), ctypes.byref(c),
+                                  B, hq, T, off, kv, qp, qs, qo, k.data_ptr(), ks, v.data_ptr(), vs,
+                                  _ptr(status_ws), _raw_stream(dev))
     if rc:
         raise GdpaError(rc, w)
     return q_out
@@ -594,59 +606,67 @@ def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, sc
     ``window``, limited to the last ``window`` tokens; ``max_n`` bounds the new
     tokens of a sample.  Returns (o [T, hq, dh], lse fp32 [hq, T] or None)."""
     w = "gdpa_chunk_fwd"
-    with _On(w, q, stream) as st:
-        dev = q.device
-        _need(q.dim() == 3, w, "q: [T, hq, dh]")
-        T, hq, dh = q.shape
-        _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
-        B = offsets.numel() - 1
-        c = _cache(w, cache_k, cache_v, page_table, B)
-        _operand(w, "q", q, torch.bfloat16, (T, hq, c.dh), cache_k.device)
-        _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
-        _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _operand(w, "o", o, torch.bfloat16, (T, hq, dh), dev)
-        if lse is not None:
-            _operand(w, "lse", lse, torch.float32, (hq, T), dev)
-        elif want_lse:
-            lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = workspace(_chunk_workspace(dev.index, c.hk, c.dh, hq, max_n), dev)
-        else:
-            _need(ws.is_cuda and ws.device == dev and ws.dtype == torch.uint8
-                  and ws.is_contiguous(), w, "ws: a contiguous uint8 tensor on the device")
-        rc = load().gdpa_chunk_fwd(ctypes.byref(c), B, hq, T, max_n,
-                                   0x7fffffff if window is None else window, scale, _ptr(q),
-                                   _ptr(offsets), _ptr(kv_len), _ptr(o), _ptr(lse), _ptr(ws),
-                                   ws.numel(), st)
+    on = _elsewhere(w, q, stream)
+    if on:
+        with on:
+            return chunk_fwd(q, offsets, kv_len, page_table, cache_k, cache_v, scale, max_n, window, o,
+                             lse, ws, want_lse)
+    dev = q.get_device()
+    _need(q.dim() == 3, w, "q: [T, hq, dh]")
+    T, hq, dh = q.shape
+    _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
+    B = offsets.numel() - 1
+    c = _cache(w, cache_k, cache_v, page_table, B)
+    hk, cdh = cache_k.shape[1], cache_k.shape[3]
+    qp = _operand(w, "q", q, torch.bfloat16, (T, hq, cdh), cache_k.get_device())
+    off = _operand(w, "offsets", offsets, torch.int32, (B + 1,), dev)
+    kv = _operand(w, "kv_len", kv_len, torch.int32, (B,), dev)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _operand(w, "o", o, torch.bfloat16, (T, hq, dh), dev)
+    if lse is not None:
+        _operand(w, "lse", lse, torch.float32, (hq, T), dev)
+    elif want_lse:
+        lse = torch.empty((hq, T), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = workspace(_chunk_workspace(dev, hk, dh, hq, max_n), q.device)
+    else:
+        _need(ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous(), w,
+              "ws: a contiguous uint8 tensor on the device")
+    rc = load().gdpa_chunk_fwd(ctypes.byref(c), B, hq, T, max_n,
+                               0x7fffffff if window is None else window, scale, qp, off, kv,
+                               o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if rc:
         raise GdpaError(rc, w)
     return o, lse
 
 
-def _block_norm(where, x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid) -> BlockNorm:
-    """Checks the operands of a block norm and fills its description."""
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2
-          and x.dtype in (torch.bfloat16, torch.float32), where, "x: bf16 or fp32 [T, d]")
-    T, d = x.shape
-    _operand(where, "x", x, x.dtype, (T, d), x.device)
+def _block_norm(where, x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid):
+    """Checks the operands of a block norm: its description, and the addresses of
+    offsets, x, f, gate, w_post, w_pre."""
+    dt, dev = x.dtype, x.get_device()
+    _need(x.dim() == 2 and dt in (torch.bfloat16, torch.float32), where, "x: bf16 or fp32 [T, d]")
+    shape = x.shape
+    T, d = shape
+    at = [None, _operand(where, "x", x, dt, shape, dev), None, None, None, None]
     if f is not None:
-        _operand(where, "f", f, x.dtype, (T, d), x.device)
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None:
-            _operand(where, name, t, torch.float32, (d,), x.device)
+        at[2] = _operand(where, "f", f, dt, shape, dev)
     kind, B = 0, 0
     if gate is not None:
-        kind = 1 if offsets is None else 2
-        B = 0 if offsets is None else offsets.numel() - 1
-        _operand(where, "gate", gate, x.dtype, (T if kind == 1 else B, d), x.device)
-    if offsets is not None:
-        _need(gate is not None, where, "offsets go with a gate shared by a sample's rows")
-        _operand(where, "offsets", offsets, torch.int32, (B + 1,), x.device)
-    return BlockNorm(T, d, DTYPE_BF16 if x.dtype == torch.bfloat16 else DTYPE_F32, kind,
-                     int(bool(sigmoid)), B, alpha, eps, 0)
+        kind = 1
+        if offsets is not None:
+            kind, B = 2, offsets.numel() - 1
+            at[0] = _operand(where, "offsets", offsets, torch.int32, (B + 1,), dev)
+        at[3] = _operand(where, "gate", gate, dt, shape if kind == 1 else (B, d), dev)
+    else:
+        _need(offsets is None, where, "offsets go with a gate shared by a sample's rows")
+    if w_post is not None:
+        at[4] = _operand(where, "w_post", w_post, torch.float32, (d,), dev)
+    if w_pre is not None:
+        at[5] = _operand(where, "w_pre", w_pre, torch.float32, (d,), dev)
+    return BlockNorm(T, d, DTYPE_BF16 if dt is torch.bfloat16 else DTYPE_F32, kind, int(bool(sigmoid)),
+                     B, alpha, eps, 0), at
 
 
 def block_norm_fwd(x: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, offsets=None,
@@ -658,22 +678,24 @@ def block_norm_fwd(x: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, 
     without ``w_post`` f enters as it is, without ``w_pre`` there is no n, without
     ``f`` y is x.  Returns (y, n)."""
     w = "gdpa_block_norm_fwd"
-    with _On(w, x, stream) as st:
-        p = _block_norm(w, x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid)
-        if f is None:
-            _need(y is None, w, "y without f")
-        elif y is None:
-            y = torch.empty_like(x)
-        else:
-            _operand(w, "y", y, x.dtype, tuple(x.shape), x.device)
-        if w_pre is None:
-            _need(n is None, w, "n without w_pre")
-        elif n is None:
-            n = torch.empty_like(x)
-        else:
-            _operand(w, "n", n, x.dtype, tuple(x.shape), x.device)
-        rc = load().gdpa_block_norm_fwd(ctypes.byref(p), _ptr(offsets), _ptr(x), _ptr(f),
-                                        _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(y), _ptr(n), st)
+    on = _elsewhere(w, x, stream)
+    if on:
+        with on:
+            return block_norm_fwd(x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid, y, n)
+    p, at = _block_norm(w, x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid)
+    if f is None:
+        _need(y is None, w, "y without f")
+    elif y is None:
+        y = torch.empty_like(x)
+    else:
+        _operand(w, "y", y, x.dtype, x.shape, x.get_device())
+    if w_pre is None:
+        _need(n is None, w, "n without w_pre")
+    elif n is None:
+        n = torch.empty_like(x)
+    else:
+        _operand(w, "n", n, x.dtype, x.shape, x.get_device())
+    rc = load().gdpa_block_norm_fwd(ctypes.byref(p), *at, _ptr(y), _ptr(n), _raw_stream(x.get_device()))
     if rc:
         raise GdpaError(rc, w)
     return (x if f is None else y), n
@@ -686,35 +708,50 @@ def block_norm_bwd(y: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, 
     x where there is no f); returns (dx, df, dgate, dw_post, dw_pre), None where
     there is no such operand.  dgate of a sample gate is fp32 [B, d]."""
     w = "gdpa_block_norm_bwd"
+    on = _elsewhere(w, y, stream)
+    if on:
+        with on:
+            return block_norm_bwd(y, f, gate, w_post, w_pre, dy, dn, offsets, alpha, eps, sigmoid, dx,
+                                  df, dgate, ws)
     lib = load()
-    with _On(w, y, stream) as st:
-        p = _block_norm(w, y, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid)
-        shape, dev = tuple(y.shape), y.device
-        _need((dn is None) == (w_pre is None), w, "dn goes with w_pre")
-        for name, t in (("dy", dy), ("dn", dn)):
-            if t is not None:
-                _operand(w, name, t, y.dtype, shape, dev)
-        dx = torch.empty_like(y) if dx is None else dx
-        _operand(w, "dx", dx, y.dtype, shape, dev)
-        if f is not None:
-            df = torch.empty_like(y) if df is None else df
-            _operand(w, "df", df, y.dtype, shape, dev)
-        if gate is not None:
-            gt = torch.float32 if offsets is not None else y.dtype
-            if dgate is None:
-                dgate = torch.empty(gate.shape, dtype=gt, device=dev)
-            _operand(w, "dgate", dgate, gt, tuple(gate.shape), dev)
-        dw_post, dw_pre = (None if t is None else torch.empty_like(t) for t in (w_post, w_pre))
-        n = ctypes.c_size_t()
-        rc = lib.gdpa_block_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n))
-        if rc:
-            raise GdpaError(rc, "gdpa_block_norm_bwd_workspace_size")
-        if ws is None:
-            ws = workspace(n.value, dev)
-        rc = lib.gdpa_block_norm_bwd(ctypes.byref(p), _ptr(offsets), _ptr(y), _ptr(f), _ptr(gate),
-                                     _ptr(w_post), _ptr(w_pre), _ptr(dy), _ptr(dn), _ptr(dx),
-                                     _ptr(df), _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
-                                     ws.numel(), st)
+    p, at = _block_norm(w, y, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid)
+    dt, shape, dev = y.dtype, y.shape, y.get_device()
+    _need((dn is None) == (w_pre is None), w, "dn goes with w_pre")
+    if dy is not None:
+        _operand(w, "dy", dy, dt, shape, dev)
+    if dn is not None:
+        _operand(w, "dn", dn, dt, shape, dev)
+    if dx is None:
+        dx = torch.empty_like(y)
+    else:
+        _operand(w, "dx", dx, dt, shape, dev)
+    if f is None:
+        _need(df is None, w, "df without f")
+    elif df is None:
+        df = torch.empty_like(y)
+    else:
+        _operand(w, "df", df, dt, shape, dev)
+    if gate is None:
+        _need(dgate is None, w, "dgate without a gate")
+    else:
+        gt = torch.float32 if offsets is not None else dt
+        if dgate is None:
+            dgate = torch.empty(gate.shape, dtype=gt, device=y.device)
+        else:
+            _operand(w, "dgate", dgate, gt, gate.shape, dev)
+    dw_post, dw_pre = (None if t is None else torch.empty_like(t) for t in (w_post, w_pre))
+    n = ctypes.c_size_t()
+    rc = lib.gdpa_block_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n))
+    if rc:
+        raise GdpaError(rc, "gdpa_block_norm_bwd_workspace_size")
+    if ws is None:
+        ws = workspace(n.value, y.device)
+    else:
+        _need(ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous(), w,
+              "ws: a contiguous uint8 tensor on the device")
+    rc = lib.gdpa_block_norm_bwd(ctypes.byref(p), *at, _ptr(dy), _ptr(dn), dx.data_ptr(), _ptr(df),
+                                 _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), ws.data_ptr(), ws.numel(),
+                                 _raw_stream(dev))
     if rc:
         raise GdpaError(rc, w)
     return dx, df, dgate, dw_post, dw_pre
