@@ -449,10 +449,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 class _On:
     """Makes a device current, and `stream` (when given) the stream that allocations
-    belong to, for the length of a call."""
+    belong to, for the length of a call; the allocator keeps the call's tensors until that stream
+    has passed it."""
 
-    def __init__(self, dev, stream):
+    def __init__(self, dev, stream, tensors):
         self.ctx = [torch.cuda.device(dev)]
+        self.tensors = tensors if stream is not None else ()
         if stream is not None:
             if not isinstance(stream, torch.cuda.Stream):
                 raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -462,18 +464,21 @@ class _On:
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
+        for t in self.tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(torch.cuda.current_stream())
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
 
 
-def _elsewhere(where, t, stream) -> Optional[_On]:
-    """What a call on `t` and `stream` has to run under; None where it is in force already."""
+def _elsewhere(where, t, stream, *more) -> Optional[_On]:
+    """What a call on `t` (and `more` tensors) and `stream` has to run under; None where it is in force already."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise GdpaError(1, f"{where} (a CUDA tensor)")
     dev = t.get_device()
-    return None if stream is None and dev == _current_device() else _On(dev, stream)
+    return None if stream is None and dev == _current_device() else _On(dev, stream, (t, *more))
 
 
 def rotary_spec(rot: int, base: float = 10000.0, interleaved: bool = False, factor: float = 1.0,
@@ -495,7 +500,7 @@ def rotary(spec: RotarySpec, x: torch.Tensor, offsets=None, kv_len=None, positio
     ``out`` may be ``x``; rows behind the last sample are left as they were (in a
     new ``out``: not set).  ``inverse`` gives the gradient."""
     w = "gdpa_rotary"
-    on = _elsewhere(w, x, stream)
+    on = _elsewhere(w, x, stream, offsets, kv_len, positions, out)
     if on:
         with on:
             return rotary(spec, x, offsets, kv_len, positions, out, inverse)
@@ -544,7 +549,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, offsets, kv_len, page_table, 
     ``kv_len`` [B] counts each sample's tokens with the new ones.  With ``q``
     [T, hq, dh] its rotation is returned (``q_out``)."""
     w = "gdpa_cache_append"
-    on = _elsewhere(w, cache_k, stream)
+    on = _elsewhere(w, cache_k, stream, k, v, offsets, kv_len, page_table, cache_v, q, q_out, status_ws)
     if on:
         with on:
             return cache_append(k, v, offsets, kv_len, page_table, cache_k, cache_v, spec, q, q_out,
@@ -606,7 +611,7 @@ def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, sc
     ``window``, limited to the last ``window`` tokens; ``max_n`` bounds the new
     tokens of a sample.  Returns (o [T, hq, dh], lse fp32 [hq, T] or None)."""
     w = "gdpa_chunk_fwd"
-    on = _elsewhere(w, q, stream)
+    on = _elsewhere(w, q, stream, offsets, kv_len, page_table, cache_k, cache_v, o, lse, ws)
     if on:
         with on:
             return chunk_fwd(q, offsets, kv_len, page_table, cache_k, cache_v, scale, max_n, window, o,
@@ -678,7 +683,7 @@ def block_norm_fwd(x: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, 
     without ``w_post`` f enters as it is, without ``w_pre`` there is no n, without
     ``f`` y is x.  Returns (y, n)."""
     w = "gdpa_block_norm_fwd"
-    on = _elsewhere(w, x, stream)
+    on = _elsewhere(w, x, stream, f, gate, w_post, w_pre, offsets, y, n)
     if on:
         with on:
             return block_norm_fwd(x, f, gate, w_post, w_pre, offsets, alpha, eps, sigmoid, y, n)
@@ -708,7 +713,7 @@ def block_norm_bwd(y: torch.Tensor, f=None, gate=None, w_post=None, w_pre=None, 
     x where there is no f); returns (dx, df, dgate, dw_post, dw_pre), None where
     there is no such operand.  dgate of a sample gate is fp32 [B, d]."""
     w = "gdpa_block_norm_bwd"
-    on = _elsewhere(w, y, stream)
+    on = _elsewhere(w, y, stream, f, gate, w_post, w_pre, dy, dn, offsets, dx, df, dgate, ws)
     if on:
         with on:
             return block_norm_bwd(y, f, gate, w_post, w_pre, dy, dn, offsets, alpha, eps, sigmoid, dx,

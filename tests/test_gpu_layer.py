@@ -412,6 +412,18 @@ def test_calls_on_another_stream():
         s.synchronize()
         assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(n, wn) and torch.equal(r, wr)
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    # inputs that are dropped right behind the call live on until the stream has read them
+    big = torch.randn(1 << 20, 96, device=DEV)
+    want = G.block_norm_fwd(big, w_pre=w)[1]
+    copy = big.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    _, n = G.block_norm_fwd(copy, w_pre=w, stream=s)
+    del copy
+    torch.zeros(1 << 20, 96, device=DEV)
+    s.synchronize()
+    assert torch.equal(n, want)
 
 
 def test_empty_batch():
