@@ -240,7 +240,7 @@ __device__ __forceinline__ void row_sum_w(float (&v)[K], int W, int wi, int gi, 
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if (W == 1) return;
-  float* b = buf + flip * (kWarpsFwd * 3) + gi * W * K;
+  float* b = buf + flip * (kWarpsFwd * 6) + gi * W * K;
   flip ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -263,7 +263,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
   constexpr int P = Co::P;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarpsFwd * kStages];
-  __shared__ float buf[2 * 3 * kWarpsFwd];
+  __shared__ float buf[2 * 6 * kWarpsFwd];
   __shared__ int abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (blockDim.x / 32 / W) + gi;
@@ -391,7 +391,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
   constexpr int P = Co::P;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarpsFwd * kStages];
-  __shared__ float buf[2 * 3 * kWarpsFwd];
+  __shared__ float buf[2 * 6 * kWarpsFwd];
   __shared__ int abort_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gi = warp / W, wi = warp - gi * W, g = blockIdx.x * (blockDim.x / 32 / W) + gi;
@@ -512,46 +512,67 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
       st.next(t, lane);
       continue;
     }
-    // the row into registers, with the sums of y^2, w_pre dn y and f^2
-    float2 q[3] = {two(0.f), two(0.f), two(0.f)};
+    // The row into registers, with all the sums of its two norms at once: of y^2, w_pre dn y and f^2, and, with
+    // s = act w_post f, of s dy, s w_pre dn and s y, of which mean(w_post du fh) is made (G is linear in them),
+    // so that nothing of the row waits for a second sum.
+    float2 q[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) q[k] = two(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (Co::any(i, lane, n)) {
+        float2 wn[P], s[P];
         Co::shared(st.at(0), i, lane, n, G[i]);
+        if (!a.dy)
+#pragma unroll
+          for (int k = 0; k < P; ++k) G[i][k] = two(0.f);
         if constexpr (PRE) {
-          float2 w[P];
           Co::shared(st.at(KY), i, lane, n, y[i]);
           Co::shared(st.at(KN), i, lane, n, dn[i]);
-          Co::weights(a.w_pre + col0, i, lane, n, w);
+          Co::weights(a.w_pre + col0, i, lane, n, wn);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
+            wn[k] = __fmul2_rn(wn[k], dn[i][k]);
             q[0] = __ffma2_rn(y[i][k], y[i][k], q[0]);
-            q[1] = __ffma2_rn(__fmul2_rn(dn[i][k], w[k]), y[i][k], q[1]);
+            q[1] = __ffma2_rn(wn[k], y[i][k], q[1]);
           }
         }
         if constexpr (BLOCK) Co::shared(st.at(KF), i, lane, n, f[i]);
-        if constexpr (POST)
-#pragma unroll
-          for (int k = 0; k < P; ++k) q[2] = __ffma2_rn(f[i][k], f[i][k], q[2]);
         if constexpr (GATE == GDPA_GATE_TOKEN) {
           Co::shared(st.at(KZ), i, lane, n, z[i]);
           act(z[i], a.sigmoid, slope[i]);
         }
+        if constexpr (POST) {
+          if constexpr (!SHARED) Co::weights(a.w_post + col0, i, lane, n, s);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            if constexpr (SHARED) s[k] = z[i][k];             // (act w_post)
+            if constexpr (GATE == GDPA_GATE_TOKEN) s[k] = __fmul2_rn(s[k], z[i][k]);
+            s[k] = __fmul2_rn(s[k], f[i][k]);
+            q[2] = __ffma2_rn(f[i][k], f[i][k], q[2]);
+            q[3] = __ffma2_rn(s[k], G[i][k], q[3]);
+            if constexpr (PRE) {
+              q[4] = __ffma2_rn(s[k], wn[k], q[4]);
+              q[5] = __ffma2_rn(s[k], y[i][k], q[5]);
+            }
+          }
+        }
       }
     }
     st.next(t, lane);
-    float v[3] = {q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y};
-    if constexpr (PRE || POST) row_sum_w(v, W, wi, gi, buf, flip);
+    constexpr int K = POST ? PRE ? 6 : 4 : 2;
+    float v[6];
+#pragma unroll
+    for (int k = 0; k < 6; ++k) v[k] = q[k].x + q[k].y;
+    if constexpr (PRE || POST) row_sum_w(*reinterpret_cast<float(*)[K]>(v), W, wi, gi, buf, flip);
     const float sy = poison * rsqrtf(fmaf(v[0], a.inv_d, a.eps));
     const float my = v[1] * sy * a.inv_d;                  // mean(w_pre dn yh)
     const float sf = POST ? rsqrtf(fmaf(v[2], a.inv_d, a.eps)) : 1.f;
-    float2 m2v = two(0.f);
+    // mean(w_post du fh)
+    const float mf = a.alpha * sf * a.inv_d * (PRE ? fmaf(sy, fmaf(-my * sy, v[5], v[4]), v[3]) : v[3] * poison);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (Co::any(i, lane, n)) {
-        if (!a.dy)
-#pragma unroll
-          for (int k = 0; k < P; ++k) G[i][k] = two(0.f);
         if constexpr (PRE) {
           float2 w[P];
           Co::weights(a.w_pre + col0, i, lane, n, w);
@@ -566,52 +587,32 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
           for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(poison));
         }
         Co::put(reinterpret_cast<E*>(a.dx) + t * a.d + col0, i, lane, n, G[i]);
-        if constexpr (BLOCK)           // from here on G holds alpha G, then alpha act w_post G; f holds fh
-#pragma unroll
-          for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(a.alpha));
-        if constexpr (POST) {
-          float2 w[P];
-          if constexpr (!SHARED) Co::weights(a.w_post + col0, i, lane, n, w);
+        if constexpr (BLOCK) {         // G: alpha G, alpha act w_post G (without act for a token gate's slope), df
+          float2 w[P], dz[P];
+          if constexpr (POST && !SHARED) Co::weights(a.w_post + col0, i, lane, n, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
-            f[i][k] = __fmul2_rn(f[i][k], two(sf));
-            const float2 e = __fmul2_rn(G[i][k], f[i][k]);
-            if constexpr (SHARED) {
-              agate[i][k] = __fadd2_rn(agate[i][k], e);
-              m2v = __ffma2_rn(e, z[i][k], m2v);
-              G[i][k] = __fmul2_rn(G[i][k], z[i][k]);
-            } else {
-              float2 ez = e;
-              if constexpr (GATE == GDPA_GATE_TOKEN) ez = __fmul2_rn(e, z[i][k]);
-              apost[i][k] = __fadd2_rn(apost[i][k], ez);
-              m2v = __ffma2_rn(ez, w[k], m2v);
+            G[i][k] = __fmul2_rn(G[i][k], two(a.alpha));
+            if constexpr (POST) f[i][k] = __fmul2_rn(f[i][k], two(sf));
+            float2 e = __fmul2_rn(G[i][k], f[i][k]);                    // alpha G fh
+            if constexpr (SHARED) agate[i][k] = __fadd2_rn(agate[i][k], e);
+            if constexpr (GATE != GDPA_GATE_NONE) G[i][k] = __fmul2_rn(G[i][k], z[i][k]);
+            if constexpr (POST && !SHARED) {
               G[i][k] = __fmul2_rn(G[i][k], w[k]);
+              apost[i][k] = GATE == GDPA_GATE_TOKEN ? __ffma2_rn(e, z[i][k], apost[i][k])
+                                                    : __fadd2_rn(apost[i][k], e);
             }
-          }
-        }
-      }
-    }
-    float m2[1] = {m2v.x + m2v.y};
-    if constexpr (POST) row_sum_w(m2, W, wi, gi, buf, flip);
-    const float mf = m2[0] * a.inv_d;
-    if constexpr (BLOCK)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        if (Co::any(i, lane, n)) {
-          float2 dz[P];
-#pragma unroll
-          for (int k = 0; k < P; ++k) {
-            if constexpr (GATE == GDPA_GATE_TOKEN)                      // alpha G u act'
-              dz[k] = __fmul2_rn(__fmul2_rn(G[i][k], f[i][k]), slope[i][k]);
-            if constexpr (SHARED && !POST)
-              agate[i][k] = __ffma2_rn(G[i][k], f[i][k], agate[i][k]);
-            if constexpr (GATE == GDPA_GATE_TOKEN || (SHARED && !POST)) G[i][k] = __fmul2_rn(G[i][k], z[i][k]);
+            if constexpr (GATE == GDPA_GATE_TOKEN) {                    // alpha G u act'
+              if constexpr (POST) e = __fmul2_rn(e, w[k]);
+              dz[k] = __fmul2_rn(e, slope[i][k]);
+            }
             if constexpr (POST) G[i][k] = __fmul2_rn(two(sf), __ffma2_rn(f[i][k], two(-mf), G[i][k]));
           }
           Co::put(reinterpret_cast<E*>(a.df) + t * a.d + col0, i, lane, n, G[i]);
           if constexpr (GATE == GDPA_GATE_TOKEN) Co::put(reinterpret_cast<E*>(a.dgate) + t * a.d + col0, i, lane, n, dz);
         }
       }
+    }
   }
   if (SHARED && st.t1 > st.t0) flush();
   // the block's weight gradients: its groups in order, through shared memory (every copy has been read)
