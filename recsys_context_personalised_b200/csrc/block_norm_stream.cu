@@ -438,9 +438,9 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
   SampleWalk walk;
   walk.next = -1;
   walk.b = 0;
-  // act(gate) of this thread's columns: of this row, or of this sample (times w_post)
+  // the gate of this thread's columns: a sample's act(gate) (times w_post), or a row's gate as it is (act
+  // is taken twice rather than kept with its slope: registers)
   float2 z[GATE != GDPA_GATE_NONE ? NV : 1][P];
-  float2 slope[GATE == GDPA_GATE_TOKEN ? NV : 1][P];          // act'(gate)
   // the rows of sample walk.b that this group holds are done: their gate gradient goes out whole, or as
   // a piece (slot 1 when it holds the sample's first row)
   auto flush = [&]() {
@@ -540,14 +540,19 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
         if constexpr (BLOCK) Co::shared(st.at(KF), i, lane, n, f[i]);
         if constexpr (GATE == GDPA_GATE_TOKEN) {
           Co::shared(st.at(KZ), i, lane, n, z[i]);
-          act(z[i], a.sigmoid, slope[i]);
         }
         if constexpr (POST) {
+          float2 az[P];
+          if constexpr (GATE == GDPA_GATE_TOKEN) {
+#pragma unroll
+            for (int k = 0; k < P; ++k) az[k] = z[i][k];
+            act(az, a.sigmoid);
+          }
           if constexpr (!SHARED) Co::weights(a.w_post + col0, i, lane, n, s);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             if constexpr (SHARED) s[k] = z[i][k];             // (act w_post)
-            if constexpr (GATE == GDPA_GATE_TOKEN) s[k] = __fmul2_rn(s[k], z[i][k]);
+            if constexpr (GATE == GDPA_GATE_TOKEN) s[k] = __fmul2_rn(s[k], az[k]);
             s[k] = __fmul2_rn(s[k], f[i][k]);
             q[2] = __ffma2_rn(f[i][k], f[i][k], q[2]);
             q[3] = __ffma2_rn(s[k], G[i][k], q[3]);
@@ -589,6 +594,8 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
         Co::put(reinterpret_cast<E*>(a.dx) + t * a.d + col0, i, lane, n, G[i]);
         if constexpr (BLOCK) {         // G: alpha G, alpha act w_post G (without act for a token gate's slope), df
           float2 w[P], dz[P];
+          float2 slope[P];
+          if constexpr (GATE == GDPA_GATE_TOKEN) act(z[i], a.sigmoid, slope);
           if constexpr (POST && !SHARED) Co::weights(a.w_post + col0, i, lane, n, w);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
@@ -604,7 +611,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
             }
             if constexpr (GATE == GDPA_GATE_TOKEN) {                    // alpha G u act'
               if constexpr (POST) e = __fmul2_rn(e, w[k]);
-              dz[k] = __fmul2_rn(e, slope[i][k]);
+              dz[k] = __fmul2_rn(e, slope[k]);
             }
             if constexpr (POST) G[i][k] = __fmul2_rn(two(sf), __ffma2_rn(f[i][k], two(-mf), G[i][k]));
           }

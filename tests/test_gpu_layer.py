@@ -565,6 +565,15 @@ def test_norm_streamed_rows(dtype, d, gate, post, pre):
     _check_norm([2000, 0, 1, 2900], d, dtype, gate, post, pre, seed=d, pad=7 if gate == "sample" else 0)
 
 
+@pytest.mark.parametrize("n,d,dtype", [([9000, 0, 3], 7, torch.bfloat16), ([4500, 4501], 64, torch.bfloat16),
+                                       ([9001], 100, torch.float32), ([300, 0, 400], 4100, torch.float32),
+                                       ([300, 0, 400], 8191, torch.float32)])
+@pytest.mark.parametrize("gate", ["token", "sample"])
+def test_norm_rows_in_registers(n, d, dtype, gate):
+    """Many narrow rows and very wide ones, several to a group of threads."""
+    _check_norm(n, d, dtype, gate, seed=d, pad=3 if gate == "sample" else 0)
+
+
 @pytest.mark.parametrize("std", [0.0, 1e-6, 1e6])
 def test_norm_scales(std):
     """Rows of zeros (the root holds eps alone), tiny and huge rows."""
