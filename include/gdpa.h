@@ -324,9 +324,10 @@ GDPA_API gdpa_status_t gdpa_window_bwd(int32_t B, int32_t h, int32_t dh, int64_t
  * of keys and values for serving, attention of new tokens over that cache,
  * and the norms around a block.  The Kunlun pages name the sequence's
  * self-attention only (section 2.2, sliding-window bullet); these calls are
- * what a layer of it needs in training and in serving.  They read offsets as
- * the calls above do, except that rows t >= offsets[B] (a padded batch) are
- * allowed: such rows of an output are left as they were.
+ * what a layer of it needs in training and in serving.  offsets [B+1] (device)
+ * must not decrease; rows t < offsets[0] or t >= offsets[B] (a padded batch) are
+ * allowed: such rows of an output are left as they were.  (gdpa_chunk_fwd reports
+ * offsets that break this; the other calls give undefined values for them, within their tensors.)
  */
 
 /*

@@ -6,7 +6,7 @@
 // bytes in flight (about 100 KB an SM) do not depend on what the arithmetic holds, and a row's
 // reductions are shuffles within a warp, or a barrier of a row's few warps, that no other row waits for.
 // Measured (copy: 6.5 TB/s): 132 k rows of 2048 bf16 with a gate per element forward 447 us, 6.1 TB/s; 126 k rows
-// of 1024 backward, with a gate per element 360 us, 5.7 TB/s, with shared gates 330 us, 4.7 TB/s.
+// of 1024 backward, with a gate per element 364 us, 5.7 TB/s, with shared gates 280 us, 5.5 TB/s.
 //
 // The weights' gradients (and a shared gate's) accumulate in fp32 registers over the range, in the
 // rows' order, and go to the workspace once.

@@ -30,7 +30,8 @@
 //
 // The code is kept short and its rare parts out of line: a launch fetches it cold, and the warps
 // waited for instructions most of the time with separate masked and unmasked paths
-// (0.28 ms for 48 sessions of up to 700 events in a 256-event window, against 0.14 ms).
+// (48 sessions of up to 700 events in a 256-event window 0.28 ms, in this form 0.14 ms, and 0.12 ms with the masks
+// by bit tests).
 #include <limits.h>
 #include <math.h>
 

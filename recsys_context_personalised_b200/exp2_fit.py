@@ -9,20 +9,19 @@ deg + 2 reference points, move the references to the extrema of the error
 curve, repeat until they settle).
 
 ``python exp2_fit.py`` prints the coefficients rounded to fp32 and the error
-bound; csrc/gdpa_internal.cuh holds the same numbers.  csrc/chunk_sm100.cu takes n as
-the nearest integer, f in [-1/2, 1/2], and a quintic.
+bound; csrc/gdpa_internal.cuh holds the same numbers.
 """
 from __future__ import annotations
 
 import numpy as np
 
 
-def remez_exp2(deg: int = 3, iters: int = 40, grid: int = 200001, lo: float = 0.0):
-    """Coefficients c0..c_deg (low order first) and the max relative error on [lo, lo + 1]."""
+def remez_exp2(deg: int = 3, iters: int = 40, grid: int = 200001):
+    """Coefficients c0..c_deg (low order first) and the max relative error."""
     n = deg + 2
-    xs = np.linspace(lo, lo + 1.0, grid)
+    xs = np.linspace(0.0, 1.0, grid)
     fx = np.exp2(xs)
-    ref = lo + 0.5 - 0.5 * np.cos(np.pi * np.arange(n) / (n - 1))   # Chebyshev points
+    ref = 0.5 - 0.5 * np.cos(np.pi * np.arange(n) / (n - 1))   # Chebyshev points on [0, 1]
     c = None
     for _ in range(iters):
         A = np.zeros((n, n))
@@ -53,6 +52,3 @@ if __name__ == "__main__":
     coef, bound = remez_exp2()
     print("c0..c3 (fp32):", [float(np.float32(v)) for v in coef])
     print("max relative error on [0, 1]:", bound)
-    coef, bound = remez_exp2(5, lo=-0.5)
-    print("c0..c5 (fp32):", [float(np.float32(v)) for v in coef])
-    print("max relative error on [-1/2, 1/2]:", bound)
