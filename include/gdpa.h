@@ -419,7 +419,8 @@ GDPA_API gdpa_status_t gdpa_cache_append(const gdpa_rotary_t* r, const gdpa_cach
  *   multiple of hk, hq / hk <= 128.  max_n: upper bound of the n_b (selects the kernel).
  *   Cache rows that no new token of the sample sees may hold anything (NaN too), and pages
  *   without such rows need no valid table entry.
- *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned;
+ *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned of its own
+ *   for every call that may run beside another one;
  *   its status word receives GDPA_ERR_INVALID_ARG for offsets that decrease,
  *   leave [0, T] or exceed max_n (the sample is skipped), and for a kv_len past
  *   the page table or a page outside [0, num_pages) among those it reads (the
@@ -472,7 +473,8 @@ GDPA_API gdpa_status_t gdpa_block_norm_fwd(const gdpa_block_norm_t* p, const int
  *   dx, df [T, d]; dgate [T, d] like the gate, or fp32 [B, d] for a sample gate
  *   (zero for a sample without rows); dw_post, dw_pre fp32 [d].
  *   dy may be NULL (zero) when dn is given; dn goes with w_pre.
- *   workspace: device, >= gdpa_block_norm_bwd_workspace_size bytes, 256-byte aligned.
+ *   workspace: device, >= gdpa_block_norm_bwd_workspace_size bytes, 256-byte aligned,
+ *   of its own for every call that may run beside another one.
  * Reproducible: the same inputs give the same bits (no atomics).
  */
 GDPA_API gdpa_status_t gdpa_block_norm_bwd_workspace_size(const gdpa_block_norm_t* p,

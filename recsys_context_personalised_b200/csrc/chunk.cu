@@ -36,7 +36,7 @@ struct BlockMeta {
   int32_t lo, hi;            // positions that some row of the tile sees
   int32_t pos0, tokens;      // first token's position, tokens of the tile
   int32_t token0;            // global index of the first token
-  int32_t vhead;             // kv head * vheads + part
+  int32_t kvh;               // kv head
   int32_t flags;             // kFirst | kLast of this worker's visit of the item; kBegins | kEnds of the item
 };
 enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };
@@ -141,7 +141,6 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     const int pr = min(C::kBN, 1 << a.page_shift);          // rows of a page piece
     const int pieces = C::kBN / pr;
-    const int heads = a.hk * a.vheads;
     int b = start.b;
     ChunkPlace at = start.at;
     int32_t token0 = 0;
@@ -155,20 +154,19 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int nb = s.blocks(at.tile);
       const int lo = s.lo(at.tile), hi = s.hi(at.tile), kb0 = s.first_block(at.tile);
       const int tokens = s.tokens(at.tile), i0 = at.tile * s.rt;
-      const int kvh = at.head / a.vheads, part = at.head - kvh * a.vheads;
       if (fresh) {
         begins = at.block == 0;
-        // Q of the item: `vgroup` heads of `rt` tokens (rows past the item are never stored)
+        // Q of the item: the kv head's `group` heads of `rt` tokens (rows past the item are never stored)
         const uint32_t qs = qn % C::QST, qph = (qn / C::QST) & 1u;
         ok = mbar_wait(bar(C::B_QEMPTY + qs), qph ^ 1u, abort_flag, kChunkTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          mbar_expect_tx(bar(C::B_QFULL + qs), (uint32_t)(a.rt * a.vgroup) * DH * 2);
+          mbar_expect_tx(bar(C::B_QFULL + qs), (uint32_t)(a.rt * a.group) * DH * 2);
 #pragma unroll
           for (int c = 0; c < C::NCH; ++c)
             tma_load_3d(base + C::OFF_Q + qs * C::QB + c * C::QCHUNKB, &tmQ, bar(C::B_QFULL + qs),
-                        c * C::CH, kvh * a.group + part * a.vgroup, token0 + i0);
+                        c * C::CH, at.head * a.group, token0 + i0);
         }
         ++qn;
       }
@@ -203,7 +201,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             m.pos0 = s.ctx + i0;
             m.tokens = tokens;
             m.token0 = token0 + i0;
-            m.vhead = at.head;
+            m.kvh = at.head;
             m.flags = (fresh ? kFirst : 0) | (begins ? kBegins : 0) |
                       (at.block == nb - 1 ? kEnds : 0) |
                       (at.block == nb - 1 || left == 1 ? kLast : 0);
@@ -218,7 +216,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (pc < pieces && (mask >> pc & 1u))
           tma_load_4d(base + C::OFF_KV + slot * C::SLOTB + c * C::CHUNKB + pc * pr * C::ROWB,
                       kv ? &tmV : &tmK, bar(C::B_KVFULL + slot), c * C::CH,
-                      (key0 + pc * pr) & ((1 << a.page_shift) - 1), kvh, id);
+                      (key0 + pc * pr) & ((1 << a.page_shift) - 1), at.head, id);
         if (++slot == (uint32_t)C::NS) {
           slot = 0;
           phase ^= 1u;
@@ -232,7 +230,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         fresh = true;
         if (++at.tile == s.tiles()) {
           at.tile = 0;
-          if (++at.head == heads) {
+          if (++at.head == a.hk) {
             at.head = 0;
             if (left > 0) {
               do {
@@ -277,7 +275,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int x = 0; x < 2; ++x) {
             mx[mt][x] = -INFINITY;
             sum[mt][x] = 0.f;
-            pos[mt][x] = m.pos0 + (mt * 16 + x * 8 + g8) / a.vgroup;
+            pos[mt][x] = m.pos0 + (mt * 16 + x * 8 + g8) / a.group;
           }
 #pragma unroll
           for (int n = 0; n < DH / 8; ++n)
@@ -439,9 +437,7 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
       arrive(C::B_JOIN);
       if (!wait(C::B_JOIN, merges & 1u)) break;
-      const int kvh = m.vhead / a.vheads, part = m.vhead - kvh * a.vheads;
-      const int head0 = kvh * a.group + part * a.vgroup;
-      const int nh = min(a.vgroup, a.group - part * a.vgroup);
+      const int head0 = m.kvh * a.group;
       const bool whole = (m.flags & kBegins) && (m.flags & kEnds);
       // a piece that holds the item's first block is the part's last, else its first
       const int64_t at = 2 * worker + ((m.flags & kBegins) ? 1 : 0);
@@ -450,7 +446,6 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         pc.token0 = m.token0;
         pc.tokens = m.tokens;
         pc.head0 = head0;
-        pc.heads = nh;
         pc.ends = (m.flags & kEnds) ? 1 : 0;
         a.piece[at] = pc;
       }
@@ -458,8 +453,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll 1
       for (int e = threadIdx.x; e < C::R * DH / 4; e += kWarps * 32) {
         const int r = whole ? e / (DH / 4) : e % C::R, c4 = whole ? e % (DH / 4) : e / C::R;
-        const int tk = r / a.vgroup, h = r - tk * a.vgroup;
-        if (tk >= m.tokens || h >= nh) continue;
+        const int tk = r / a.group, h = r - tk * a.group;
+        if (tk >= m.tokens) continue;
         float2 ml[kWarps];
         float top = -INFINITY, l = 0.f;
 #pragma unroll
@@ -547,8 +542,8 @@ chunk_join_kernel(const ChunkArgs a, WsHeader* ws) {
   const ChunkPiece first = a.piece[2 * w + 1];
   const int cg = warp % GROUPS, sp = warp / GROUPS, r8 = lane & 7, c4 = lane >> 3;
   const int r = blockIdx.y * 8 + r8, x = r / a.tile_rows, rr = r - x * a.tile_rows;
-  const int tk = rr / a.vgroup, h = rr - tk * a.vgroup;
-  const bool live = tk < a.rt1 && x * a.rt1 + tk < first.tokens && h < first.heads;
+  const int tk = rr / a.group, h = rr - tk * a.group;
+  const bool live = tk < a.rt1 && x * a.rt1 + tk < first.tokens;
   if (!__any_sync(0xffffffffu, live)) return;                 // (the same in every warp of the block)
   // worker of the item's last piece: the next one that holds the item's end
   int last = w + 1;
@@ -621,7 +616,7 @@ cudaError_t launch_rows(const ChunkArgs& a, const gdpa_cache_t& c, cudaStream_t 
 // How a call is cut.  `tiles`: the tcgen05 kernel of chunk_sm100.cu.
 struct ChunkLayout {
   bool tiles;
-  int mt, rows, tile_rows, vheads, vgroup, rt1, rt, workers;
+  int mt, rows, tile_rows, rt1, rt, workers;
   size_t status_off, piece_off, ml_off, po_off, total;
 };
 ChunkLayout chunk_layout(const gdpa_cache_t& c, int hq, int max_n) {
@@ -636,9 +631,7 @@ ChunkLayout chunk_layout(const gdpa_cache_t& c, int hq, int max_n) {
   L.mt = need <= 16 ? 1 : 2;
   L.tile_rows = L.tiles ? 128 : 16 * L.mt;
   L.rows = L.tiles ? 256 : L.tile_rows;
-  L.vheads = (group + L.tile_rows - 1) / L.tile_rows;
-  L.vgroup = (group + L.vheads - 1) / L.vheads;
-  L.rt1 = L.tile_rows / L.vgroup;
+  L.rt1 = L.tile_rows / group;        // (0 only where max_n is: no rows)
   L.rt = L.tiles ? 2 * L.rt1 : L.rt1;
   L.workers = (L.tiles ? 1 : 2) * device_sm_count();
   L.status_off = sizeof(WsHeader);
@@ -681,7 +674,7 @@ bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int b
   const cuuint64_t row = (cuuint64_t)dh * 2;
   const cuuint64_t qsize[3] = {(cuuint64_t)dh, (cuuint64_t)a.hq, (cuuint64_t)a.T};
   const cuuint64_t qstride[2] = {row, a.hq * row};
-  const cuuint32_t qbox[3] = {(cuuint32_t)ch, (cuuint32_t)a.vgroup, (cuuint32_t)a.rt1};
+  const cuuint32_t qbox[3] = {(cuuint32_t)ch, (cuuint32_t)a.group, (cuuint32_t)a.rt1};
   const cuuint64_t size[4] = {(cuuint64_t)dh, (cuuint64_t)c.page, (cuuint64_t)c.hk,
                               (cuuint64_t)c.num_pages};
   const cuuint64_t stride[3] = {row, c.page * row, (cuuint64_t)c.hk * c.page * row};
@@ -699,7 +692,7 @@ cudaError_t launch_join(const ChunkArgs& a, WsHeader* ws, cudaStream_t st) {
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st) {
   // few items leave many pieces to each (about workers / items): 512 threads share them
   const int64_t tiles = a.T / a.rt > a.B ? a.T / a.rt : a.B;
-  const bool many = tiles * a.hk * a.vheads * 8 < a.workers;
+  const bool many = tiles * a.hk * 8 < a.workers;
   if (dh == 32) return many ? launch_join<32, 8>(a, ws, st) : launch_join<32, 1>(a, ws, st);
   if (dh == 64) return many ? launch_join<64, 4>(a, ws, st) : launch_join<64, 1>(a, ws, st);
   return many ? launch_join<128, 2>(a, ws, st) : launch_join<128, 1>(a, ws, st);
@@ -753,8 +746,6 @@ extern "C" gdpa_status_t gdpa_chunk_fwd(const gdpa_cache_t* cache, int32_t B, in
   a.hq = hq;
   a.hk = cache->hk;
   a.group = hq / cache->hk;
-  a.vheads = L.vheads;
-  a.vgroup = L.vgroup;
   a.max_n = max_n;
   a.window = window;
   a.rt = L.rt;

@@ -21,10 +21,9 @@ constexpr int chunk_rows_shift(int dh) { return dh == 128 ? 6 : dh == 64 ? 7 : 8
 // tokens = 0).  Its rows' (max in log2 units, sum) and unnormalised O are at the
 // same index of the workspace's ml and po arrays.
 struct __align__(16) ChunkPiece {
-  // row r of a tile: token r / vgroup of the tile, head head0 + r % vgroup (< head0 + heads)
-  int32_t token0, tokens, head0, heads;
+  // row r of a tile: token r / group of the tile, head head0 + r % group
+  int32_t token0, tokens, head0;
   int32_t ends;                           // this piece holds the item's last block
-  int32_t pad[3];
 };
 
 struct ChunkArgs {
@@ -39,7 +38,7 @@ struct ChunkArgs {
   float2* ml;                // [2 * workers, rows]
   float* po;                 // [2 * workers, dh / 4, rows, 4]
   int64_t T;
-  int32_t B, hq, hk, vheads, group, vgroup;   // group = hq / hk, in vheads parts of vgroup heads
+  int32_t B, hq, hk, group;  // group = hq / hk
   int32_t max_n, window, bn_shift;
   int32_t rt, rt1, rows, tile_rows;           // an item: rt tokens in tiles of rt1 tokens, rows in tiles of tile_rows
   int32_t num_pages, max_pages, page_shift;
@@ -91,13 +90,12 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, int worker, Chunk
   const int tid = threadIdx.x, nt = blockDim.x, warp = tid >> 5, lane = tid & 31;
   const int run = (a.B + nt - 1) / nt;
   const int b0 = min(a.B, tid * run), b1 = min(a.B, b0 + run);
-  const int heads = a.hk * a.vheads;
   int64_t mine = 0;
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
     int32_t t0;
     const ChunkSample s = load_sample(a, b, t0, bad);
-    if (s.n > 0) mine += s.blocks_before(s.tiles()) * heads;
+    if (s.n > 0) mine += s.blocks_before(s.tiles()) * a.hk;
   }
   int64_t upto = mine;
 #pragma unroll
@@ -125,7 +123,7 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, int worker, Chunk
       int32_t t0;
       const ChunkSample s = load_sample(a, b, t0, bad);
       if (s.n == 0) continue;
-      const int64_t w = s.blocks_before(s.tiles()) * heads;
+      const int64_t w = s.blocks_before(s.tiles()) * a.hk;
       if (x0 < lo + w) {
         out->count = x1 - x0;
         out->b = b;
@@ -138,7 +136,7 @@ __device__ __forceinline__ void find_start(const ChunkArgs& a, int worker, Chunk
   __syncthreads();
 }
 
-// The tensor maps of a call: Q as boxes of rt1 tokens x vgroup heads, K and V
+// The tensor maps of a call: Q as boxes of rt1 tokens x group heads, K and V
 // as boxes of the rows of a page that lie in one block of `bn` positions; `ch` elements wide.
 bool chunk_maps(const ChunkArgs& a, const gdpa_cache_t& c, int dh, int ch, int bn,
                 CUtensorMapSwizzle sw, CUtensorMap* q, CUtensorMap* k, CUtensorMap* v);

@@ -51,7 +51,7 @@ struct __align__(16) Visit {
   int32_t b0[2], b1[2];      // blocks of it that tile A / B sees
   int32_t pos0, token0;      // position and global index of the first token
   int32_t tok[2];            // tokens of tile A / B
-  int32_t vhead, flags;
+  int32_t kvh, flags;
 };
 enum { kBegins = 1, kEnds = 2 };   // the item's first / last block is among them
 
@@ -206,7 +206,6 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       // ---------------------------------------------------------- producer
       const int pr = min(kBNT, 1 << a.page_shift);            // rows of a page piece
       const int pieces = kBNT / pr;
-      const int heads = a.hk * a.vheads;
       int b = start.b;
       ChunkPlace at = start.at;
       int32_t token0 = 0;
@@ -221,7 +220,7 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         const int nb = s.blocks(at.tile), first = s.first_block(at.tile);
         const int take = (int)min((int64_t)(nb - at.block), left);
         const int lo = s.lo(at.tile), hi = s.hi(at.tile), i0 = at.tile * s.rt;
-        const int kvh = at.head / a.vheads, part = at.head - kvh * a.vheads;
+        const int kvh = at.head;
         const int u0 = first + at.block, u1 = u0 + take;
         const uint32_t qs = vn % C::QST;
         ok = mbar_wait(bar(C::B_QEMPTY + qs), ((vn / C::QST) & 1u) ^ 1u, abort_flag, kChunkTimeoutNs);
@@ -245,20 +244,20 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             v.b1[x] = some ? min(u1, ((h - 1) >> kBNTShift) + 1) : 0;
             if (v.b1[x] <= v.b0[x]) v.b0[x] = v.b1[x] = 0;
           }
-          v.vhead = at.head;
+          v.kvh = kvh;
           v.flags = (at.block == 0 ? kBegins : 0) | (at.block + take == nb ? kEnds : 0);
           visits[qs] = v;
           const bool two = v.tok[1] > 0;
-          const uint32_t qb = (uint32_t)(a.rt1 * a.vgroup) * DH * 2;
+          const uint32_t qb = (uint32_t)(a.rt1 * a.group) * DH * 2;
           const uint32_t qaddr = sQ + qs * 2 * C::TILEB;
           mbar_expect_tx(bar(C::B_QFULL + qs), two ? 2 * qb : qb);
 #pragma unroll
           for (int c = 0; c < C::NCH; ++c) {
             tma_load_3d(qaddr + c * C::CHUNKB, &tmQ, bar(C::B_QFULL + qs), c * C::CH,
-                        kvh * a.group + part * a.vgroup, token0 + i0);
+                        kvh * a.group, token0 + i0);
             if (two)
               tma_load_3d(qaddr + C::TILEB + c * C::CHUNKB, &tmQ, bar(C::B_QFULL + qs), c * C::CH,
-                          kvh * a.group + part * a.vgroup, token0 + i0 + a.rt1);
+                          kvh * a.group, token0 + i0 + a.rt1);
           }
         }
         __syncwarp();
@@ -310,7 +309,7 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
           at.block = 0;
           if (++at.tile == s.tiles()) {
             at.tile = 0;
-            if (++at.head == heads) {
+            if (++at.head == a.hk) {
               at.head = 0;
               if (left > 0) {
                 do {
@@ -466,7 +465,7 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const uint32_t my_s = tmem + lane_off + C::COL_S + 128 * x;
     const uint32_t my_o = tmem + lane_off + C::COL_O + DH * x;
-    const int tk = row / a.vgroup, hd = row - tk * a.vgroup;
+    const int tk = row / a.group, hd = row - tk * a.group;
     // |scale| (S holds the products of -Q for a negative one); of a zero scale so little is kept that
     // every logit is 0 and a masked one still -inf
     const float c2 = fmaxf(fabsf(a.scale_log2), 1e-30f);
@@ -484,11 +483,9 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
       const int tokens = x ? v.tok[1] : v.tok[0];
       if (tokens <= 0) continue;
       const int j0 = x ? v.b0[1] : v.b0[0], j1 = x ? v.b1[1] : v.b1[0];
-      const int kvh = v.vhead / a.vheads, part = v.vhead - kvh * a.vheads;
-      const int head0 = kvh * a.group + part * a.vgroup;
-      const int nh = min(a.vgroup, a.group - part * a.vgroup);
-      const bool store = tk < tokens && hd < nh;
-      const bool dead = quad * 32 >= tokens * a.vgroup;       // no row of this warp is stored
+      const int head0 = v.kvh * a.group;
+      const bool store = tk < tokens;
+      const bool dead = quad * 32 >= tokens * a.group;       // no row of this warp is stored
       // the row sees the positions [low, pos]; the whole warp sees [wlow, wpos]
       const int pos = v.pos0 + x * a.rt1 + tk;
       const int low = (int)max((int64_t)pos - window + 1, (int64_t)0);
@@ -600,7 +597,6 @@ chunk_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
         pc.token0 = v.token0;
         pc.tokens = v.tok[0] + v.tok[1];
         pc.head0 = head0;
-        pc.heads = nh;
         pc.ends = (v.flags & kEnds) ? 1 : 0;
         a.piece[at] = pc;
       }

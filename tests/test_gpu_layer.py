@@ -745,6 +745,48 @@ def test_a_served_step_captured_and_replayed():
         assert torch.equal(y, ey) and torch.equal(n, en) and torch.equal(y2, ey) and torch.equal(n2, en)
 
 
+@pytest.mark.parametrize("d", [96, 512])
+def test_training_operators_captured_and_replayed(d):
+    """Rotary and its gradient, block norm and its gradient in two graphs that are replayed in turn with
+    other inputs and other offsets in the same buffers: the bits of eager calls."""
+    B, T, spec = 4, 300, G.rotary_spec(32, base=1e4)
+    dev = {k: _dev(v) for k, v in _norm_case(T, d, torch.bfloat16, "sample", True, True, 31, B=B)[0].items()}
+    off = _int32([0, 100, 100, 170, 300])
+    gen = torch.Generator(device=DEV).manual_seed(32)
+
+    def fill():
+        for k in ("x", "f", "gate"):
+            dev[k].normal_(generator=gen)
+    dn = torch.randn(T, d, device=DEV, generator=gen).bfloat16()
+
+    def step():
+        x = G.rotary(spec, dev["x"].view(T, d // 32, 32), offsets=off).view(T, d)
+        y, n = G.block_norm_fwd(x, dev["f"], dev["gate"], dev["w_post"], dev["w_pre"], off, sigmoid=True)
+        g = G.block_norm_bwd(y, dev["f"], dev["gate"], dev["w_post"], dev["w_pre"], n, dn, off, sigmoid=True)
+        back = G.rotary(spec, g[0].view(T, d // 32, 32), offsets=off, inverse=True)
+        return (x, y, n, back, *g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    outs = []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(step())
+    for places in ([0, 100, 100, 170, 300], [0, 0, 1, 299, 300], [0, 300, 300, 300, 300]):
+        fill()
+        off.copy_(_int32(places))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_a_training_layer_and_its_gradient():
     """norm -> rotary -> window attention -> gated residual and back: the gradient of the residual stream
     against fp64 autograd of the same layer (dense causal window), within the bf16 activations' roundings."""
