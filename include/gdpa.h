@@ -419,7 +419,7 @@ GDPA_API gdpa_status_t gdpa_cache_append(const gdpa_rotary_t* r, const gdpa_cach
  *   multiple of hk, hq / hk <= 128.  max_n: upper bound of the n_b (selects the kernel).
  *   Cache rows that no new token of the sample sees may hold anything (NaN too), and pages
  *   without such rows need no valid table entry.
- *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned of its own
+ *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned, of its own
  *   for every call that may run beside another one;
  *   its status word receives GDPA_ERR_INVALID_ARG for offsets that decrease,
  *   leave [0, T] or exceed max_n (the sample is skipped), and for a kv_len past
