@@ -335,16 +335,19 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 1));
             big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 2));
           }
-          // the running max moves only when it grew by more than 2^8 (softmax does
-          // not depend on the offset, and 2^8 is far from overflow)
-          const bool move = big[0] > mx[mt][0] + 8.f || big[1] > mx[mt][1] + 8.f;
-          if (__any_sync(0xffffffffu, move)) {
+          // a row's offset moves only when its maximum grew by more than 2^8 (softmax does
+          // not depend on the offset, and 2^8 is far from overflow).  Each row decides for itself, and one that stays
+          // is scaled by exactly 1: the tile's rows behind the item hold what was there before (or other
+          // samples' queries) and must not change a bit of the others
+          bool move[2];
+#pragma unroll
+          for (int row = 0; row < 2; ++row) move[row] = big[row] > mx[mt][row] + 8.f;
+          if (__any_sync(0xffffffffu, move[0] || move[1])) {
             float f[2];
 #pragma unroll
             for (int row = 0; row < 2; ++row) {
-              const float to = fmaxf(mx[mt][row], big[row]);
-              f[row] = to == -INFINITY ? 1.f : ex2_approx(mx[mt][row] - to);
-              mx[mt][row] = to;
+              f[row] = move[row] ? ex2_approx(mx[mt][row] - big[row]) : 1.f;
+              if (move[row]) mx[mt][row] = big[row];
               sum[mt][row] *= f[row];
             }
 #pragma unroll
