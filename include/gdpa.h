@@ -416,7 +416,9 @@ GDPA_API gdpa_status_t gdpa_cache_append(const gdpa_rotary_t* r, const gdpa_cach
  * position) gets O = 0 and LSE = -inf.
  *   q, o bf16 [T, hq, dh]; lse fp32 [hq, T] (may be NULL); offsets, kv_len as in
  *   gdpa_cache_append.  window >= 1 (2^31 - 1: plain causal attention).  hq a
- *   multiple of hk, hq / hk <= 128.  max_n: upper bound of the n_b (selects the kernel).
+ *   multiple of hk, hq / hk <= 128.  max_n: upper bound of the n_b (selects the kernel); rows that belong
+ *   to no sample do not count, so T may exceed B * max_n.  gdpa_chunk_workspace_size takes the samples' tokens
+ *   alone, at most B * max_n (its result does not depend on them).
  *   Cache rows that no new token of the sample sees may hold anything (NaN too), and pages
  *   without such rows need no valid table entry.
  *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned, of its own

@@ -629,12 +629,12 @@ ChunkLayout chunk_layout(const gdpa_cache_t& c, int hq, int max_n) {
   // tiles on the tensor core's tcgen05 path beyond that.  At dh = 128 a thread has no registers for 32 rows of O
   // beside the rest: 32 rows over 8 x 15 k positions, 8 kv heads, took 199 us in one tile of 32 and 100 us on the
   // tcgen05 path (dh = 64: 75 and 83 us).
-  const int64_t need = (int64_t)group * max_n;
+  const int64_t need = (int64_t)group * (max_n > 1 ? max_n : 1);   // (0: a batch of padding alone)
   L.tiles = need > (c.dh == 128 ? 16 : 32);
   L.mt = need <= 16 ? 1 : 2;
   L.tile_rows = L.tiles ? 128 : 16 * L.mt;
   L.rows = L.tiles ? 256 : L.tile_rows;
-  L.rt1 = L.tile_rows / group;        // (0 only where max_n is: no rows)
+  L.rt1 = L.tile_rows / group;
   L.rt = L.tiles ? 2 * L.rt1 : L.rt1;
   L.workers = (L.tiles ? 1 : 2) * device_sm_count();
   L.status_off = sizeof(WsHeader);
@@ -648,9 +648,7 @@ ChunkLayout chunk_layout(const gdpa_cache_t& c, int hq, int max_n) {
 gdpa_status_t check_chunk(const gdpa_cache_t* c, int32_t B, int32_t hq, int64_t T, int32_t max_n) {
   const gdpa_status_t s = check_cache(c, B);
   if (s != GDPA_OK) return s;
-  if (hq < 1 || hq % c->hk || T < 0 || T >= (int64_t)1 << 31 || max_n < 0 ||
-      (int64_t)max_n * B < T)
-    return GDPA_ERR_INVALID_ARG;
+  if (hq < 1 || hq % c->hk || T < 0 || T >= (int64_t)1 << 31 || max_n < 0) return GDPA_ERR_INVALID_ARG;
   if (hq / c->hk > 128 || (int64_t)hq * c->dh > (1 << 20)) return GDPA_ERR_UNSUPPORTED;
   return GDPA_OK;
 }
@@ -693,8 +691,10 @@ cudaError_t launch_join(const ChunkArgs& a, WsHeader* ws, cudaStream_t st) {
                           dim3(DH / 16 * SPLIT * 32), st, a, ws);
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, int dh, WsHeader* ws, cudaStream_t st) {
-  // few items leave many pieces to each (about workers / items): 512 threads share them
-  const int64_t tiles = a.T / a.rt > a.B ? a.T / a.rt : a.B;
+  // few items leave many pieces to each (about workers / items): 512 threads share them.  (Rows behind the last
+  // sample are none of the at most B * max_n tokens.)
+  const int64_t most = (int64_t)a.B * a.max_n, tokens = a.T < most ? a.T : most;
+  const int64_t tiles = tokens / a.rt > a.B ? tokens / a.rt : a.B;
   const bool many = tiles * a.hk * 8 < a.workers;
   if (dh == 32) return many ? launch_join<32, 8>(a, ws, st) : launch_join<32, 1>(a, ws, st);
   if (dh == 64) return many ? launch_join<64, 4>(a, ws, st) : launch_join<64, 1>(a, ws, st);
@@ -709,7 +709,7 @@ extern "C" gdpa_status_t gdpa_chunk_workspace_size(const gdpa_cache_t* cache, in
                                                    int64_t T, int32_t max_n, size_t* bytes) {
   const gdpa_status_t s = check_chunk(cache, B, hq, T, max_n);
   if (s != GDPA_OK) return s;
-  if (!bytes) return GDPA_ERR_INVALID_ARG;
+  if (!bytes || (int64_t)max_n * B < T) return GDPA_ERR_INVALID_ARG;   // (the samples' tokens)
   *bytes = chunk_layout(*cache, hq, max_n).total;
   return GDPA_OK;
 }

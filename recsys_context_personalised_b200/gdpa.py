@@ -590,8 +590,9 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, offsets, kv_len, page_table, 
 
 
 def chunk_workspace_bytes(cache: Cache, B: int, hq: int, T: int, max_n: int) -> int:
+    """Workspace of a chunk_fwd call on T rows (those behind the last sample, which do not count, among them)."""
     n = ctypes.c_size_t()
-    rc = load().gdpa_chunk_workspace_size(ctypes.byref(cache), B, hq, T, max_n, ctypes.byref(n))
+    rc = load().gdpa_chunk_workspace_size(ctypes.byref(cache), B, hq, min(T, B * max_n), max_n, ctypes.byref(n))
     if rc:
         raise GdpaError(rc, "gdpa_chunk_workspace_size")
     return n.value
@@ -609,7 +610,8 @@ def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, sc
     """Run gdpa_chunk_fwd: attention of the new tokens q [T, hq, dh] over each
     sample's ``kv_len`` cached tokens (its own among them), causal and, with
     ``window``, limited to the last ``window`` tokens; ``max_n`` bounds the new
-    tokens of a sample.  Returns (o [T, hq, dh], lse fp32 [hq, T] or None)."""
+    tokens of a sample (rows of a padded batch that belong to none do not count, and stay as they were: in a
+    new ``o`` not set).  Returns (o [T, hq, dh], lse fp32 [hq, T] or None)."""
     w = "gdpa_chunk_fwd"
     on = _elsewhere(w, q, stream, offsets, kv_len, page_table, cache_k, cache_v, o, lse, ws)
     if on:

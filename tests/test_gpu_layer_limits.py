@@ -1,5 +1,5 @@
 """The attention layer's operators at the edges of their calls, on the GPU: rows of a tile that no token
-owns.  Helpers: test_gpu_layer."""
+owns, padded batches.  Helpers: test_gpu_layer."""
 import pytest
 import torch
 
@@ -51,3 +51,45 @@ def test_a_sample_keeps_its_bits_beside_other_neighbours(group, n, dh):
         loud[off[keep]:] *= 40
         o, lse = G.chunk_fwd(loud.to(DEV), *args, max_n=max(n))
         assert torch.equal(o[:off[keep]], want[:off[keep]]) and torch.equal(lse[:, :off[keep]], wl[:, :off[keep]])
+
+
+def _padded_call(off, kv, table, ck, cv, q, scale, max_n, hq):
+    """chunk_fwd into outputs full of 7: (o, lse, status)."""
+    T, dh = q.shape[0], q.shape[2]
+    args = (_int32(off), _int32(kv), _int32(table), ck.to(DEV), cv.to(DEV))
+    o = torch.full((T, hq, dh), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((hq, T), 7.0, device=DEV)
+    c = G._cache("t", args[3], args[4], args[2], len(kv))
+    ws = G.workspace(G.chunk_workspace_bytes(c, len(kv), hq, T, max_n), DEV)
+    G.chunk_fwd(q.to(DEV), *args, scale, max_n=max_n, o=o, lse=lse, ws=ws)
+    return o, lse, G.workspace_status(ws)
+
+
+@pytest.mark.parametrize("dh,hq,hk", [(64, 4, 2), (128, 8, 1), (32, 40, 1)])
+@pytest.mark.parametrize("n", [[1, 1, 1], [0, 1, 0], [2, 0, 3]])
+@pytest.mark.parametrize("before,behind", [(0, 61), (5, 0), (3, 200)])
+def test_a_padded_batch(n, dh, hq, hk, before, behind):
+    """Few tokens in many rows, with the true bound of the lengths: the bits of the call without the padding,
+    whose rows stay as they were."""
+    kv = [300, 61, 1200]
+    off, _, table, ck, cv, q, scale = _chunk_case(n, kv, hq, hk, dh, 16, 44)
+    want, wl, _ = _padded_call(off, kv, table, ck, cv, q, scale, max(n), hq)
+    T = off[-1]
+    pads = [torch.full((m, hq, dh), float("nan"), dtype=q.dtype) for m in (before, behind)]
+    wide = torch.cat([pads[0], q, pads[1]])
+    o, lse, status = _padded_call([before + x for x in off], kv, table, ck, cv, wide, scale, max(n), hq)
+    assert status == 0
+    mine = slice(before, before + T)
+    assert torch.equal(o[mine], want) and torch.equal(lse[:, mine], wl)
+    o[mine], lse[:, mine] = 7.0, 7.0
+    assert (o == 7.0).all() and (lse == 7.0).all()
+
+
+@pytest.mark.parametrize("hq", [1, 20, 128])
+def test_a_batch_of_padding_alone(hq):
+    """No sample has a token and max_n says so: nothing is written; a sample with a token is then reported."""
+    off, _, table, ck, cv, q, scale = _chunk_case([0, 0], [40, 0], hq, 1, 64, 16, 45, pad=9)
+    o, lse, status = _padded_call(off, [40, 0], table, ck, cv, q, scale, 0, hq)
+    assert status == 0 and (o == 7.0).all() and (lse == 7.0).all()
+    o, lse, status = _padded_call([0, 1, 1], [40, 0], table, ck, cv, q, scale, 0, hq)
+    assert status == 1 and (o == 7.0).all() and (lse == 7.0).all()

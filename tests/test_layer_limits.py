@@ -1,0 +1,32 @@
+"""The attention layer's operators at the edges of their calls: what the host accepts and refuses (CPU only: no call
+here reaches a kernel launch)."""
+import ctypes
+
+import pytest
+
+from recsys_context_personalised_b200 import gdpa as G
+from test_layer_plan import P, _cache
+
+
+@pytest.mark.parametrize("B,T,max_n", [(3, 64, 1), (1, 1000, 4), (2, 10, 0)])
+def test_a_padded_batch_is_not_refused(B, T, max_n):
+    """Rows behind the last sample do not count against max_n, the bound of a sample's tokens: the call goes on
+    to its workspace (5: too small), whose size does not depend on them."""
+    lib, c = G.load(), _cache()
+    assert lib.gdpa_chunk_fwd(ctypes.byref(c), B, 4, T, max_n, 8, 1.0, P, P, P, P, None, P, 0, None) == 5
+    assert G.chunk_workspace_bytes(c, B, 4, T, max_n) == G.chunk_workspace_bytes(c, B, 4, 0, max_n)
+    for bad in (dict(T=-1), dict(T=1 << 31), dict(max_n=-1), dict(B=0)):
+        kw = {**dict(B=B, T=T, max_n=max_n), **bad}
+        assert lib.gdpa_chunk_fwd(ctypes.byref(c), kw["B"], 4, kw["T"], kw["max_n"], 8, 1.0, P, P, P, P, None, P,
+                                  1 << 40, None) == 1
+        if kw["T"] < 1 << 31:
+            with pytest.raises(G.GdpaError):
+                G.chunk_workspace_bytes(c, kw["B"], 4, kw["T"], kw["max_n"])
+
+
+@pytest.mark.parametrize("group", [1, 16, 17, 40, 128])
+def test_a_bound_of_zero_takes_the_workspace_of_one(group):
+    lib, c, n = G.load(), _cache(hk=1), [ctypes.c_size_t(), ctypes.c_size_t()]
+    for max_n in (0, 1):
+        assert lib.gdpa_chunk_workspace_size(ctypes.byref(c), 2, group, 0, max_n, ctypes.byref(n[max_n])) == 0
+    assert n[0].value == n[1].value
