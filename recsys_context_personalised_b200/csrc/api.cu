@@ -6,7 +6,7 @@
 #include <string>
 #include <vector>
 
-#include "gdpa_internal.cuh"
+#include "layer_launch.cuh"
 
 namespace gdpa {
 

@@ -2,7 +2,7 @@
 // block_norm_stream.cu: rows streamed through shared memory).
 #pragma once
 
-#include "gdpa_internal.cuh"
+#include "layer_launch.cuh"
 
 namespace gdpa {
 

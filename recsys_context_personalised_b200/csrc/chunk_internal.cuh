@@ -5,7 +5,7 @@
 #include <cudaTypedefs.h>
 
 #include "chunk_plan.cuh"
-#include "gdpa_internal.cuh"
+#include "layer_launch.cuh"
 #include "sm100.cuh"
 
 namespace gdpa {

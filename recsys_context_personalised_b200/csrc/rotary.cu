@@ -18,7 +18,7 @@
 #include <math.h>
 #include <stdio.h>
 
-#include "gdpa_internal.cuh"
+#include "layer_launch.cuh"
 #include "paged.cuh"
 
 namespace gdpa {

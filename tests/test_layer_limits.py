@@ -1,6 +1,7 @@
 """The attention layer's operators at the edges of their calls: what the host accepts and refuses (CPU only: no call
 here reaches a kernel launch)."""
 import ctypes
+import importlib
 
 import pytest
 
@@ -30,3 +31,12 @@ def test_a_bound_of_zero_takes_the_workspace_of_one(group):
     for max_n in (0, 1):
         assert lib.gdpa_chunk_workspace_size(ctypes.byref(c), 2, group, 0, max_n, ctypes.byref(n[max_n])) == 0
     assert n[0].value == n[1].value
+
+
+@pytest.mark.parametrize("kernel", ["gdpa_fwd_sm100", "gdpa_bwd_sm100"])
+def test_the_recorded_traffic_belongs_to_the_present_sources(kernel):
+    """The bench reports a kernel's DRAM bytes while the sources that they were captured with are unchanged: what
+    other operators share stands in headers that these kernels do not include."""
+    bench = importlib.import_module("bench")
+    for workload, (per_unit, _) in bench.TRAFFIC_PER_UNIT[kernel].items():
+        assert bench.traffic_for(kernel, workload, 2.0) == 2.0 * per_unit
