@@ -462,7 +462,8 @@ typedef struct {
  *   the last sample are left as they were).  w_post, w_pre fp32 [d].  y may be x.
  *   f NULL (then no gate, w_post, y): n = w_pre * x / rms(x).  w_pre NULL: no n.
  *   Base pointers 16-byte aligned (offsets 4-byte).
- * Statistics and sums are fp32, and n is taken from y before y is rounded.
+ * Statistics and sums are fp32, and n is taken from y before y is rounded.  There is no status word: of a row that
+ * does not arrive within a wait's limit (2 s), and of those behind it, what was not computed is NaN.
  */
 GDPA_API gdpa_status_t gdpa_block_norm_fwd(const gdpa_block_norm_t* p, const int32_t* offsets,
                                            const void* x, const void* f, const void* gate,
@@ -476,7 +477,8 @@ GDPA_API gdpa_status_t gdpa_block_norm_fwd(const gdpa_block_norm_t* p, const int
  *   (zero for a sample without rows); dw_post, dw_pre fp32 [d].
  *   dy may be NULL (zero) when dn is given; dn goes with w_pre.
  *   workspace: device, >= gdpa_block_norm_bwd_workspace_size bytes, 256-byte aligned,
- *   of its own for every call that may run beside another one.
+ *   of its own for every call that may run beside another one; its status word receives
+ *   GDPA_ERR_TIMEOUT when a row did not arrive within a wait's limit (what depends on it is NaN).
  * Reproducible: the same inputs give the same bits (no atomics).
  */
 GDPA_API gdpa_status_t gdpa_block_norm_bwd_workspace_size(const gdpa_block_norm_t* p,
@@ -490,7 +492,7 @@ GDPA_API gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const int
                                            void* stream);
 
 /*
- * Device-detected status of the last gdpa_fwd/gdpa_bwd that used `workspace`
+ * Device-detected status of the last call that used `workspace`
  * (GDPA_OK, GDPA_ERR_INVALID_ARG for inconsistent offsets, GDPA_ERR_TIMEOUT).
  * Synchronises `stream`; writes the code to *status (host).
  */
@@ -535,6 +537,15 @@ GDPA_API int32_t gdpa_timing_read(gdpa_kernel_time_t* out, int32_t cap);
  */
 GDPA_API gdpa_status_t gdpa_selftest_wait_timeout(void* workspace, size_t workspace_bytes,
                                                   uint32_t timeout_us, void* stream);
+
+/*
+ * Self-test of the block norm's waits.  In the next gdpa_block_norm_fwd or _bwd call that this thread launches (if its
+ * form streams rows through shared memory) a part of the first row of the range of rows that holds `row` never
+ * arrives, and no wait is longer than timeout_us microseconds (1 .. 5,000,000): the call ends, with NaN in place of
+ * what it could not compute, the backward with GDPA_ERR_TIMEOUT in its workspace, and the context stays usable.
+ * Later calls are not affected.  The Kunlun pages have no counterpart of this call.
+ */
+GDPA_API gdpa_status_t gdpa_selftest_norm_wait(int64_t row, uint32_t timeout_us);
 
 /*
  * Self-test of the FMA-pipe exp2 that the softmax kernels use for part of

@@ -364,11 +364,19 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormArgs a, 
 }
 
 // Adds up the partial weight gradients (blockIdx.y = 0: post, 1: pre), 32 columns to a block of
-// 32 x 32 threads, and (blockIdx.y = 2) joins the pieces of the sample gates' gradients.
+// 32 x 32 threads, and (blockIdx.y = 2) joins the pieces of the sample gates' gradients.  The first block also
+// takes the streamed blocks' status words together into the workspace's.
 __global__ void __launch_bounds__(1024)
-norm_join_kernel(const NormArgs a, float* dw_post, float* dw_pre, int blocks) {
+norm_join_kernel(const NormArgs a, float* dw_post, float* dw_pre, int blocks, WsHeader* ws) {
   __shared__ float s[32][33];
   pdl_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int worst = GDPA_OK;
+    if (a.status)
+      for (int i = threadIdx.x; i < blocks; i += blockDim.x) worst |= a.status[i];
+    worst = __syncthreads_or(worst);
+    if (threadIdx.x == 0) ws->status = worst ? GDPA_ERR_TIMEOUT : GDPA_OK;
+  }
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   if (blockIdx.y < 2) {
     const float* part = blockIdx.y ? a.part_pre : a.part_post;
@@ -445,11 +453,25 @@ Plan plan(int64_t T, int d, int dtype, bool backward, int gate_kind) {
   return p;
 }
 
-size_t ws_bytes(const Plan& p, int d, int gate_kind) {
-  size_t n = align_up((size_t)p.blocks * d * 4, 256) * 2;
-  if (gate_kind == GDPA_GATE_SAMPLE) n += align_up((size_t)p.groups * 2 * d * 4, 256);
-  return align_up(n, 256);
+// Workspace of the backward: the header, the blocks' status words and partial sums, the pieces of sample gates.
+struct NormSpace {
+  size_t status, post, pre, gate, total;
+};
+NormSpace norm_space(const Plan& p, int d, int gate_kind) {
+  const size_t part = align_up((size_t)p.blocks * d * 4, 256);
+  NormSpace w;
+  w.status = sizeof(WsHeader);
+  w.post = w.status + align_up((size_t)p.blocks * 4, 256);
+  w.pre = w.post + part;
+  w.gate = w.pre + part;
+  w.total = w.gate + (gate_kind == GDPA_GATE_SAMPLE ? align_up((size_t)p.groups * 2 * d * 4, 256) : 0);
+  return w;
 }
+
+constexpr uint64_t kNormTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy wait is microseconds
+// What gdpa_selftest_norm_wait has left for this thread's next call.
+thread_local int64_t next_lost_row = -1;
+thread_local uint64_t next_wait_ns = kNormTimeoutNs;
 
 template <typename E, int VEC, int NV>
 cudaError_t launch_fwd(const NormArgs& a, const Plan& p, cudaStream_t st) {
@@ -510,6 +532,10 @@ NormArgs base_args(const gdpa_block_norm_t* p) {
   a.inv_d = 1.f / (float)p->d;
   a.gate_kind = p->gate;
   a.sigmoid = p->sigmoid != 0;
+  a.lost_row = next_lost_row;
+  a.wait_ns = next_wait_ns;
+  next_lost_row = -1;
+  next_wait_ns = kNormTimeoutNs;
   return a;
 }
 
@@ -559,7 +585,7 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd_workspace_size(const gdpa_block_nor
   const gdpa_status_t s = check_norm(p);
   if (s != GDPA_OK) return s;
   if (!bytes) return GDPA_ERR_INVALID_ARG;
-  *bytes = ws_bytes(plan(p->T, p->d, p->dtype, true, p->gate), p->d, p->gate);
+  *bytes = norm_space(plan(p->T, p->d, p->dtype, true, p->gate), p->d, p->gate).total;
   return GDPA_OK;
 }
 
@@ -588,12 +614,12 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const i
       off16(dgate) || off16(w_post) || off16(w_pre) || off4(dw_post) || off4(dw_pre) || off4(offsets))
     return GDPA_ERR_INVALID_ARG;
   const Plan pl = plan(p->T, p->d, p->dtype, true, p->gate);
-  if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < ws_bytes(pl, p->d, p->gate))
-    return GDPA_ERR_WORKSPACE;
+  const NormSpace space = norm_space(pl, p->d, p->gate);
+  if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < space.total) return GDPA_ERR_WORKSPACE;
   const cudaStream_t st = (cudaStream_t)stream;
   if (empty) {
-    cudaError_t e = cudaSuccess;
-    if (dw_post) e = cudaMemsetAsync(dw_post, 0, (size_t)p->d * 4, st);
+    cudaError_t e = cudaMemsetAsync(workspace, 0, sizeof(WsHeader), st);
+    if (e == cudaSuccess && dw_post) e = cudaMemsetAsync(dw_post, 0, (size_t)p->d * 4, st);
     if (e == cudaSuccess && dw_pre) e = cudaMemsetAsync(dw_pre, 0, (size_t)p->d * 4, st);
     if (e == cudaSuccess && p->gate == GDPA_GATE_SAMPLE)
       e = cudaMemsetAsync(dgate, 0, (size_t)p->B * p->d * 4, st);
@@ -615,20 +641,28 @@ extern "C" gdpa_status_t gdpa_block_norm_bwd(const gdpa_block_norm_t* p, const i
   else
     a.dgate = dgate;
   a.groups = pl.groups;
-  const size_t wpart = align_up((size_t)pl.blocks * p->d * 4, 256);
-  a.part_post = w_post ? (float*)workspace : nullptr;
-  a.part_pre = w_pre ? (float*)((char*)workspace + wpart) : nullptr;
-  a.part_gate = (float*)((char*)workspace + 2 * wpart);
+  char* const ws = (char*)workspace;
+  a.status = pl.stream.nv ? (int32_t*)(ws + space.status) : nullptr;
+  a.part_post = w_post ? (float*)(ws + space.post) : nullptr;
+  a.part_pre = w_pre ? (float*)(ws + space.pre) : nullptr;
+  a.part_gate = (float*)(ws + space.gate);
   cudaError_t e = pl.stream.nv ? launch_norm_stream(a, pl.stream, p->dtype, true, st)
                   : p->dtype == GDPA_DTYPE_BF16 ? dispatch<__nv_bfloat16, 8>(a, pl, true, st)
                                                 : dispatch<float, 4>(a, pl, true, st);
-  if (e == cudaSuccess && (w_post || w_pre || p->gate == GDPA_GATE_SAMPLE)) {
+  if (e == cudaSuccess) {
     KernelScope ks_("gdpa_block_norm_join", st);
-    const int cols = (p->d + 31) / 32;
+    const int cols = w_post || w_pre ? (p->d + 31) / 32 : 1;
     const int rows = p->gate == GDPA_GATE_SAMPLE ? (p->B < 1024 ? p->B : 1024) : 0;
     e = launch_dependent(norm_join_kernel,
                          dim3(cols > rows ? cols : rows, p->gate == GDPA_GATE_SAMPLE ? 3 : 2), dim3(1024),
-                         st, a, dw_post, dw_pre, pl.blocks);
+                         st, a, dw_post, dw_pre, pl.blocks, (WsHeader*)workspace);
   }
   return finish(e);
+}
+
+extern "C" gdpa_status_t gdpa_selftest_norm_wait(int64_t row, uint32_t timeout_us) {
+  if (row < 0 || timeout_us == 0 || timeout_us > 5000000u) return GDPA_ERR_INVALID_ARG;
+  next_lost_row = row;
+  next_wait_ns = 1000ull * timeout_us;
+  return GDPA_OK;
 }

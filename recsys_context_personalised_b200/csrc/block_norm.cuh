@@ -16,7 +16,10 @@ struct NormArgs {
   float* dgate_sample;           // [B, d] (sample gates)
   float *part_post, *part_pre;   // [blocks, d] partial weight gradients
   float* part_gate;              // [groups, 2, d] partial sample-gate gradients
+  int32_t* status;               // [blocks] (streamed backward): GDPA_OK or GDPA_ERR_TIMEOUT
   int64_t T;
+  int64_t lost_row;              // -1; the self-test of the waits: a row of the group whose first row does not arrive
+  uint64_t wait_ns;              // limit of a wait
   int d, B, groups;
   float alpha, eps, inv_d;
   int gate_kind, sigmoid;

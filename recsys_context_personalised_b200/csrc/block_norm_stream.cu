@@ -25,7 +25,6 @@ using namespace sm100;
 // to three sums, for which 16 warps have too few registers and 8 hide too little (1024 wide, shared
 // gates: 496 and 458 us where 12 warps took 360).
 constexpr int kWarpsFwd = 16, kWarpsBwd = 12, kWarpsWide = 16, kMaxFwd = 2, kMaxBwd = 2;
-constexpr uint64_t kNormTimeoutNs = 2000000000ull;   // 2 s per wait; a healthy wait is microseconds
 // Rows in flight of a warp, the current one among them.  Two are enough, and what a longer ring takes is missing
 // in L1, which holds the weights: backward, 1024 wide, 4 rows 360 us, 2 rows 326 us.
 constexpr int kStages = 2;
@@ -164,6 +163,11 @@ __device__ __forceinline__ void act(float2 (&z)[P], int sigmoid, float2 (&slope)
 // The rows of one warp: its columns [col0, col0 + n) of the group's rows [t0, t1), NT tensors, in a
 // ring of kStages rows.  A copy takes whole 16-byte units: of rows that start anywhere (not AL) the units around
 // them, of the tensors' last bytes those that make a whole unit, and the rest by plain loads.
+// Waits have a limit.  A warp whose wait ran out lets the copies in flight land and copies no more, but walks through
+// its rows all the same, since the row's other warps meet it at barriers: `poison` makes its sums NaN from that row on,
+// and with them what all of the row's warps make of them.  (Each of its later waits ends at the block's
+// flag, within some 5 us.)  132 k rows of 2048 forward: 477 us without any of this, 483 in this form, 500 to 510 with a
+// branch on the wait's result in the rows' path.
 template <typename E, int NV, int NT, bool AL>
 struct Stream {
   static constexpr int VEC = 16 / sizeof(E), SEG = NV * 32 * VEC;
@@ -173,31 +177,43 @@ struct Stream {
   int64_t t0, t1, whole;        // whole: bytes of a tensor in whole units
   int d, col0, n, stage;
   uint32_t phase;
+  int limit;                    // this thread copies the rows below it (lane 0; others 0); -1: its wait ran out
+  float poison;                 // 1, or NaN
   volatile int* abort_flag;
 
   __device__ __forceinline__ int64_t first(int64_t t) const { return (t * d + col0) * (int64_t)sizeof(E); }
-  __device__ __forceinline__ void issue(int64_t t, int slot, int lane) {
-    if (t < t1 && lane == 0) {
+  __device__ __forceinline__ void issue(int64_t t, int slot, bool copy = true) {
+    if (t < limit) {
       const int64_t b0 = first(t), b1 = b0 + n * (int)sizeof(E);
       const int64_t a0 = AL ? b0 : b0 & ~(int64_t)15;
       const int64_t a1 = AL ? b1 : min((b1 + 15) & ~(int64_t)15, whole);
       const uint32_t bytes = n > 0 && a1 > a0 ? (uint32_t)(a1 - a0) : 0u;
       mbar_expect_tx(bar + 8 * slot, bytes * NT);
-      if (bytes > 0)
+      if (bytes > 0 && copy)
 #pragma unroll
         for (int k = 0; k < NT; ++k)
           bulk_load(ring + slot * ROWB + k * SEGB, reinterpret_cast<const char*>(src[k]) + a0, bytes,
                     bar + 8 * slot);
     }
   }
-  __device__ __forceinline__ void start(int lane) {
+  // (lost: the self-test of the waits; the group's first row does not come)
+  __device__ __forceinline__ void start(int lane, bool lost) {
     stage = 0;
     phase = 0;
-    for (int s = 0; s < kStages; ++s) issue(t0 + s, s, lane);
+    limit = lane == 0 ? (int)t1 : 0;
+    for (int s = 0; s < kStages; ++s) issue(t0 + s, s, !(lost && s == 0));
   }
-  // Waits for row t, the current one; false (its values are garbage) when the wait ran out.
-  __device__ __forceinline__ bool wait(int64_t t, int lane) {
-    const bool ok = mbar_wait(bar + 8 * stage, phase, abort_flag, kNormTimeoutNs);
+  // Waits for row t, the current one.
+  __device__ __forceinline__ void wait(const NormArgs& a, int64_t t, int lane) {
+    const bool ok = mbar_wait(bar + 8 * stage, phase, abort_flag, a.wait_ns);
+    if (!ok) {                  // (in some of the threads, or all)
+      if (t < limit) {
+        volatile int never = 0;
+        for (int i = 0; i < kStages && t + i < t1; ++i)
+          mbar_wait(bar + 8 * ((stage + i) % kStages), phase ^ (uint32_t)((stage + i) / kStages), &never, a.wait_ns);
+      }
+      limit = -1;
+    }
     if (!AL) {
       base = (uint32_t)(first(t) & 15);
       const int64_t b0 = first(t), b1 = b0 + n * (int)sizeof(E);
@@ -216,14 +232,14 @@ struct Stream {
         __syncwarp();
       }
     }
-    return __all_sync(0xffffffffu, ok);
+    poison = __all_sync(0xffffffffu, limit >= 0) ? 1.f : NAN;
   }
   uint32_t base = 0;            // of the row's first element in the copied units
   __device__ __forceinline__ uint32_t at(int k) const { return ring + stage * ROWB + k * SEGB + base; }
   // The current row (t) has been read: its place takes a later one.
-  __device__ __forceinline__ void next(int64_t t, int lane) {
+  __device__ __forceinline__ void next(int64_t t) {
     __syncwarp();
-    issue(t + kStages, stage, lane);
+    issue(t + kStages, stage);
     if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
@@ -285,17 +301,17 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
   st.abort_flag = &abort_s;
   st.t0 = g < a.groups ? group_row(a.T, a.groups, g) : 0;
   st.t1 = g < a.groups ? group_row(a.T, a.groups, g + 1) : 0;
-  st.start(lane);
+  st.start(lane, wi == 0 && st.t0 <= a.lost_row && a.lost_row < st.t1);
   int flip = 0;
   SampleWalk walk;
   walk.next = -1;
   walk.b = 0;
   for (int64_t t = st.t0; t < st.t1; ++t) {
-    const float poison = st.wait(t, lane) ? 1.f : NAN;
+    st.wait(a, t, lane);
     float2 y[NV][P];
     bool live = true;
     if constexpr (BLOCK) {
-      float scale = a.alpha * poison;
+      float scale = a.alpha * st.poison;
       if constexpr (POST) {
         float2 q[2] = {two(0.f), two(0.f)};
 #pragma unroll
@@ -307,7 +323,7 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
             for (int k = 0; k < P; ++k) q[k & 1] = __ffma2_rn(f[k], f[k], q[k & 1]);
           }
         }
-        float v[1] = {(q[0].x + q[1].x) + (q[0].y + q[1].y)};
+        float v[1] = {((q[0].x + q[1].x) + (q[0].y + q[1].y)) * st.poison};
         row_sum_w(v, W, wi, gi, buf, flip);
         scale *= rsqrtf(fmaf(v[0], a.inv_d, a.eps));
       }
@@ -347,11 +363,11 @@ norm_stream_fwd_kernel(const NormArgs a, int W) {
         if (Co::any(i, lane, n)) {
           Co::shared(st.at(0), i, lane, n, y[i]);
 #pragma unroll
-          for (int k = 0; k < P; ++k) y[i][k] = __fmul2_rn(y[i][k], two(poison));
+          for (int k = 0; k < P; ++k) y[i][k] = __fmul2_rn(y[i][k], two(st.poison));
         }
       }
     }
-    st.next(t, lane);
+    st.next(t);
     if (a.w_pre) {
       float2 q[2] = {two(0.f), two(0.f)};
 #pragma unroll
@@ -417,7 +433,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
   st.abort_flag = &abort_s;
   st.t0 = g < a.groups ? group_row(a.T, a.groups, g) : 0;
   st.t1 = g < a.groups ? group_row(a.T, a.groups, g + 1) : 0;
-  st.start(lane);
+  st.start(lane, wi == 0 && st.t0 <= a.lost_row && a.lost_row < st.t1);
   int flip = 0;
   float2 apost[SHARED ? 1 : NV][P], apre[NV][P], agate[SHARED ? NV : 1][P];
 #pragma unroll
@@ -485,7 +501,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
       if constexpr (GATE != GDPA_GATE_NONE) z[i][k] = two(0.f);
     }
   for (int64_t t = st.t0; t < st.t1; ++t) {
-    const float poison = st.wait(t, lane) ? 1.f : NAN;
+    st.wait(a, t, lane);
     bool live = true;
     if constexpr (SHARED) {
       if (t >= walk.next) {
@@ -509,7 +525,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
       live = walk.live(a);
     }
     if (!live) {                       // (the same for all of the row's warps) adds nothing anywhere
-      st.next(t, lane);
+      st.next(t);
       continue;
     }
     // The row into registers, with all the sums of its two norms at once: of y^2, w_pre dn y and f^2, and, with
@@ -564,17 +580,19 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
         }
       }
     }
-    st.next(t, lane);
+    st.next(t);
     constexpr int K = POST ? PRE ? 6 : 4 : 2;
     float v[6];
 #pragma unroll
     for (int k = 0; k < 6; ++k) v[k] = q[k].x + q[k].y;
+    if constexpr (PRE) v[0] *= st.poison;
+    if constexpr (POST) v[2] *= st.poison;
     if constexpr (PRE || POST) row_sum_w(*reinterpret_cast<float(*)[K]>(v), W, wi, gi, buf, flip);
-    const float sy = poison * rsqrtf(fmaf(v[0], a.inv_d, a.eps));
+    const float sy = rsqrtf(fmaf(v[0], a.inv_d, a.eps));
     const float my = v[1] * sy * a.inv_d;                  // mean(w_pre dn yh)
     const float sf = POST ? rsqrtf(fmaf(v[2], a.inv_d, a.eps)) : 1.f;
     // mean(w_post du fh)
-    const float mf = a.alpha * sf * a.inv_d * (PRE ? fmaf(sy, fmaf(-my * sy, v[5], v[4]), v[3]) : v[3] * poison);
+    const float mf = a.alpha * sf * a.inv_d * (PRE ? fmaf(sy, fmaf(-my * sy, v[5], v[4]), v[3]) : v[3]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (Co::any(i, lane, n)) {
@@ -589,7 +607,7 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(poison));
+          for (int k = 0; k < P; ++k) G[i][k] = __fmul2_rn(G[i][k], two(st.poison));
         }
         Co::put(reinterpret_cast<E*>(a.dx) + t * a.d + col0, i, lane, n, G[i]);
         if constexpr (BLOCK) {         // G: alpha G, alpha act w_post G (without act for a token gate's slope), df
@@ -622,8 +640,9 @@ norm_stream_bwd_kernel(const NormArgs a, int W) {
     }
   }
   if (SHARED && st.t1 > st.t0) flush();
-  // the block's weight gradients: its groups in order, through shared memory (every copy has been read)
+  // the block's weight gradients: its groups in order, through shared memory (every copy has landed)
   __syncthreads();
+  if (threadIdx.x == 0) a.status[blockIdx.x] = abort_s ? GDPA_ERR_TIMEOUT : GDPA_OK;
   float* sums = reinterpret_cast<float*>(smem);
   for (int which = 0; which < 2; ++which) {
     float* out = which ? a.part_pre : a.part_post;

@@ -1,10 +1,12 @@
 """The attention layer's operators at the edges of their calls, on the GPU: rows of a tile that no token
-owns, padded batches.  Helpers: test_gpu_layer."""
+owns, padded batches, waits that run out.  Helpers: test_gpu_layer."""
+import ctypes
+
 import pytest
 import torch
 
 from recsys_context_personalised_b200 import gdpa as G
-from test_gpu_layer import DEV, _chunk_case, _int32
+from test_gpu_layer import DEV, _chunk_case, _int32, _norm_case
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +95,83 @@ def test_a_batch_of_padding_alone(hq):
     assert status == 0 and (o == 7.0).all() and (lse == 7.0).all()
     o, lse, status = _padded_call([0, 1, 1], [40, 0], table, ck, cv, q, scale, 0, hq)
     assert status == 1 and (o == 7.0).all() and (lse == 7.0).all()
+
+
+# ------------------------------------------------------------------------------ waits of the streamed norm
+def _lose(row, us=3000):
+    fn = G.load().gdpa_selftest_norm_wait
+    fn.argtypes, fn.restype = [ctypes.c_int64, ctypes.c_uint32], ctypes.c_int
+    assert fn(row, us) == 0
+
+
+def _right_or_nan(got, want, what):
+    """Every element is the healthy call's or NaN; returns where it is NaN."""
+    nan = torch.isnan(got)
+    assert torch.equal(got[~nan], want[~nan]), what
+    return nan
+
+
+NORM_WAITS = [(torch.bfloat16, 200, "token", True, True), (torch.bfloat16, 2048, "sample", True, True),
+              (torch.float32, 1001, "token", True, True), (torch.bfloat16, 1001, "sample", True, False),
+              (torch.bfloat16, 8192, None, True, True), (torch.float32, 1024, None, False, True),
+              (torch.bfloat16, 5000, "token", True, False), (torch.bfloat16, 512, "token", False, False)]
+
+
+@pytest.mark.parametrize("dtype,d,gate,post,pre", NORM_WAITS)
+@pytest.mark.parametrize("T,row", [(1500, 0), (1500, 777), (3, 2)])
+def test_a_row_that_never_arrives(T, row, dtype, d, gate, post, pre):
+    """A wait that runs out ends the call with NaN in the row and no wrong number anywhere, the backward with a
+    status; the next call is whole."""
+    t, rnd = _norm_case(T, d, dtype, gate, post, pre, 46, B=2)
+    dev = {k: None if v is None else v.to(DEV) for k, v in t.items()}
+    kw = dict(offsets=_int32([0, T // 2, T]) if gate == "sample" else None, sigmoid=True)
+
+    def forward():
+        return G.block_norm_fwd(**dev, **kw)
+    y, n = forward()
+    _lose(row)
+    by, bn = forward()
+    nan = _right_or_nan(by, y, "y")
+    first = int(nan.any(1).nonzero()[0])      # the row that did not arrive, the first of those around `row`
+    assert first <= row and nan[first, 0] and (nan[first].all() or not post)
+    assert nan[row, 0] and (nan[row].all() or not post)
+    if pre:
+        assert _right_or_nan(bn, n, "n")[row].all()
+    assert all(a is None or torch.equal(a, b) for a, b in zip(forward(), (y, n)))
+
+    dy, dn = rnd(T, d).to(dtype).to(DEV), rnd(T, d).to(dtype).to(DEV) if pre else None
+    ws = G.workspace(64 << 20, DEV)
+    ws.fill_(0x5a)
+
+    def backward():
+        return G.block_norm_bwd(y, dev["f"], dev["gate"], dev["w_post"], dev["w_pre"], dy, dn, ws=ws, **kw)
+    want = backward()
+    assert G.workspace_status(ws) == 0
+    _lose(row)
+    got = backward()
+    assert G.workspace_status(ws) == 4
+    for name, a, b in zip(("dx", "df", "dgate", "dw_post", "dw_pre"), got, want):
+        if a is None:
+            continue
+        nan = _right_or_nan(a, b, name)
+        if name in ("dx", "df"):
+            assert nan[row, 0] and (nan[row].all() or not (post if name == "df" else pre)), name
+        elif name.startswith("dw"):
+            assert nan[0], name
+    again = backward()
+    assert G.workspace_status(ws) == 0
+    assert all(a is None or torch.equal(a, b) for a, b in zip(again, want))
+
+
+@pytest.mark.parametrize("T,d,dtype", [(0, 64, torch.float32), (9000, 64, torch.bfloat16), (40, 5000, torch.float32),
+                                       (40, 512, torch.bfloat16)])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, False)])
+def test_the_norms_status_word(T, d, dtype, post, pre):
+    """Set by every form: no rows, rows in registers, streamed rows; with gradients to join and without."""
+    t, rnd = _norm_case(T, d, dtype, "token", post, pre, 47)
+    dev = {k: None if v is None else v.to(DEV) for k, v in t.items()}
+    dy = rnd(T, d).to(dtype).to(DEV)
+    ws = G.workspace(64 << 20, DEV)
+    ws.fill_(0x5a)
+    G.block_norm_bwd(dev["x"], dev["f"], dev["gate"], dev["w_post"], dev["w_pre"], dy, dy if pre else None, ws=ws)
+    assert G.workspace_status(ws) == 0

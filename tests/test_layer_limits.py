@@ -40,3 +40,20 @@ def test_the_recorded_traffic_belongs_to_the_present_sources(kernel):
     bench = importlib.import_module("bench")
     for workload, (per_unit, _) in bench.TRAFFIC_PER_UNIT[kernel].items():
         assert bench.traffic_for(kernel, workload, 2.0) == 2.0 * per_unit
+
+
+def test_the_self_test_of_the_norms_waits_refuses():
+    lib = G.load()
+    fn = lib.gdpa_selftest_norm_wait
+    fn.argtypes, fn.restype = [ctypes.c_int64, ctypes.c_uint32], ctypes.c_int
+    for row, us in ((-1, 10), (0, 0), (0, 5000001)):
+        assert fn(row, us) == 1
+
+
+def test_the_norms_workspace_has_room_for_a_status():
+    """256 bytes of header for gdpa_workspace_status, and a word for every block, before anything else."""
+    lib, n = G.load(), ctypes.c_size_t()
+    for d in (8, 1024):
+        p = G.BlockNorm(1, d, 1, 0, 0, 0, 1.0, 1e-6, 0)
+        assert lib.gdpa_block_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
+        assert n.value >= 512 + 2 * 4 * d and n.value % 256 == 0
