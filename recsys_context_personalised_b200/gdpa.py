@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 from typing import Optional, Tuple
 
@@ -423,6 +424,15 @@ def _need(ok, where: str, what: str) -> None:
         raise GdpaError(1, f"{where} ({what})")
 
 
+def _i32(where: str, name: str, v) -> int:
+    """A whole number as a C int32 (ctypes would cut a longer one to its lower bits)."""
+    if type(v) is not int:
+        v = operator.index(v)
+    if v >> 31 not in (0, -1):
+        raise GdpaError(1, f"{where} ({name}: 32 bits)")
+    return v
+
+
 def _operand(where, name, t, dtype, shape, dev) -> int:
     """Address of a contiguous tensor of that type and shape on device number `dev`."""
     if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
@@ -456,6 +466,9 @@ class _On:
         self.ctx = [torch.cuda.device(dev)]
         self.tensors = tensors if stream is not None else ()
         if stream is not None:
+            at = getattr(stream, "device", None)
+            if at is not None and at.index not in (None, dev):
+                raise GdpaError(1, f"stream of {at} for tensors on cuda:{dev}")
             if not isinstance(stream, torch.cuda.Stream):
                 raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
                 stream = torch.cuda.ExternalStream(raw, device=dev)
@@ -488,8 +501,9 @@ def rotary_spec(rot: int, base: float = 10000.0, interleaved: bool = False, fact
     ``interleaved`` else (i, i + rot/2), frequencies base^(-2i/rot) divided by
     ``factor``; with ``trained_len`` only the frequencies that make fewer than
     ``high`` turns within it (fully below ``low`` turns) are."""
-    return RotarySpec(int(rot), int(bool(interleaved)), int(trained_len), 0, float(base),
-                      float(factor), float(low), float(high), float(mscale))
+    w = "rotary_spec"
+    return RotarySpec(_i32(w, "rot", int(rot)), int(bool(interleaved)), _i32(w, "trained_len", int(trained_len)), 0,
+                      float(base), float(factor), float(low), float(high), float(mscale))
 
 
 def rotary(spec: RotarySpec, x: torch.Tensor, offsets=None, kv_len=None, positions=None, out=None,
@@ -591,10 +605,11 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, offsets, kv_len, page_table, 
 
 def chunk_workspace_bytes(cache: Cache, B: int, hq: int, T: int, max_n: int) -> int:
     """Workspace of a chunk_fwd call on T rows (those behind the last sample, which do not count, among them)."""
-    n = ctypes.c_size_t()
+    n, w = ctypes.c_size_t(), "gdpa_chunk_workspace_size"
+    max_n = _i32(w, "max_n", max_n)
     rc = load().gdpa_chunk_workspace_size(ctypes.byref(cache), B, hq, min(T, B * max_n), max_n, ctypes.byref(n))
     if rc:
-        raise GdpaError(rc, "gdpa_chunk_workspace_size")
+        raise GdpaError(rc, w)
     return n.value
 
 
@@ -621,6 +636,8 @@ def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, sc
     dev = q.get_device()
     _need(q.dim() == 3, w, "q: [T, hq, dh]")
     T, hq, dh = q.shape
+    max_n = _i32(w, "max_n", max_n)
+    window = 0x7fffffff if window is None else _i32(w, "window", min(window, 0x7fffffff))   # (longer than any history)
     _need(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, w, "offsets: [B + 1]")
     B = offsets.numel() - 1
     c = _cache(w, cache_k, cache_v, page_table, B)
@@ -641,9 +658,8 @@ def chunk_fwd(q: torch.Tensor, offsets, kv_len, page_table, cache_k, cache_v, sc
     else:
         _need(ws.get_device() == dev and ws.dtype is torch.uint8 and ws.is_contiguous(), w,
               "ws: a contiguous uint8 tensor on the device")
-    rc = load().gdpa_chunk_fwd(ctypes.byref(c), B, hq, T, max_n,
-                               0x7fffffff if window is None else window, scale, qp, off, kv,
-                               o.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    rc = load().gdpa_chunk_fwd(ctypes.byref(c), B, hq, T, max_n, window, scale, qp, off, kv, o.data_ptr(),
+                               _ptr(lse), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if rc:
         raise GdpaError(rc, w)
     return o, lse

@@ -1,7 +1,8 @@
 """The attention layer's operators at the edges of their calls, on the GPU: rows of a tile that no token
-owns, padded batches, waits that run out.  Helpers: test_gpu_layer."""
+owns, padded batches, waits that run out, whole numbers beyond 32 bits.  Helpers: test_gpu_layer."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -175,3 +176,25 @@ def test_the_norms_status_word(T, d, dtype, post, pre):
     ws.fill_(0x5a)
     G.block_norm_bwd(dev["x"], dev["f"], dev["gate"], dev["w_post"], dev["w_pre"], dy, dy if pre else None, ws=ws)
     assert G.workspace_status(ws) == 0
+
+
+# ------------------------------------------------------------------------------ whole numbers beyond 32 bits
+@pytest.mark.parametrize("n", [[1, 2], [140, 3]])
+def test_windows_and_bounds_beyond_32_bits(n):
+    """A window as long as any history is plain causal attention, whatever its lower 32 bits are; numpy's whole
+    numbers are taken like Python's."""
+    kv = [300, 150]
+    off, offd, table, ck, cv, q, scale = _chunk_case(n, kv, 4, 2, 64, 16, 48)
+    args = (q.to(DEV), offd, _int32(kv), _int32(table), ck.to(DEV), cv.to(DEV), scale)
+    want, wl = G.chunk_fwd(*args, max_n=max(n))
+    for window in (2**31 - 1, 2**31, 2**32, 2**32 + 5, 2**63 - 1):
+        o, lse = G.chunk_fwd(*args, max_n=max(n), window=window)
+        assert torch.equal(o, want) and torch.equal(lse, wl), window
+    for window in (0, -1, -2**32 + 5):
+        with pytest.raises(G.GdpaError):
+            G.chunk_fwd(*args, max_n=max(n), window=window)
+    for max_n in (-1, 2**32 + max(n)):
+        with pytest.raises(G.GdpaError):
+            G.chunk_fwd(*args, max_n=max_n)
+    o, _ = G.chunk_fwd(*args, max_n=np.int64(max(n)), window=np.int32(7))
+    assert torch.equal(o, G.chunk_fwd(*args, max_n=max(n), window=7)[0])

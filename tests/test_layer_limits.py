@@ -2,8 +2,10 @@
 here reaches a kernel launch)."""
 import ctypes
 import importlib
+import types
 
 import pytest
+import torch
 
 from recsys_context_personalised_b200 import gdpa as G
 from test_layer_plan import P, _cache
@@ -57,3 +59,26 @@ def test_the_norms_workspace_has_room_for_a_status():
         p = G.BlockNorm(1, d, 1, 0, 0, 0, 1.0, 1e-6, 0)
         assert lib.gdpa_block_norm_bwd_workspace_size(ctypes.byref(p), ctypes.byref(n)) == 0
         assert n.value >= 512 + 2 * 4 * d and n.value % 256 == 0
+
+
+@pytest.mark.parametrize("kw", [dict(rot=2**32 + 64), dict(rot=64, trained_len=2**32 + 2048),
+                                dict(rot=64, trained_len=-2**32)])
+def test_rotary_settings_beyond_32_bits_are_refused(kw):
+    """A whole number that 32 bits do not hold is not cut to the ones that they do."""
+    with pytest.raises(G.GdpaError) as e:
+        G.rotary_spec(**kw)
+    assert e.value.code == 1
+
+
+def test_a_bound_beyond_32_bits_is_refused():
+    with pytest.raises(G.GdpaError) as e:
+        G.chunk_workspace_bytes(_cache(), 2, 4, 10, 2**32 + 8)
+    assert e.value.code == 1
+
+
+def test_a_stream_of_another_device_is_refused():
+    """(A stand-in for a stream: there is no device here.)"""
+    other = types.SimpleNamespace(cuda_stream=1 << 20, device=torch.device("cuda", 1))
+    with pytest.raises(G.GdpaError) as e:
+        G._On(0, other, ())
+    assert e.value.code == 1
