@@ -29,6 +29,9 @@ constexpr int kWarpsFwd = 16, kWarpsBwd = 12, kWarpsWide = 16, kMaxFwd = 2, kMax
 // in L1, which holds the weights: backward, 1024 wide, 4 rows 360 us, 2 rows 326 us.
 constexpr int kStages = 2;
 constexpr uint32_t kRingBytes = 192 * 1024;          // of a block, at most; up to 32 KB of sums come behind it
+static_assert(kStages * 5 * kWarpsWide * (kMaxBwd * 512 + 32) <= kRingBytes && kMaxFwd <= kMaxBwd &&
+                  kWarpsFwd <= kWarpsWide && kWarpsBwd <= kWarpsWide,
+              "a ring for five tensors of the widest plan");
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -724,9 +727,10 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   const int es = dtype == GDPA_DTYPE_BF16 ? 2 : 4, vec = 16 / es;
   const bool aligned = d % vec == 0;
   // Narrow rows fill few lanes of a warp: many of them are quicker in the registers' form, which puts several
-  // into a warp (14 k bf16 rows of 64 forward 4.3 and 8.6 us, of 130 already 21 and 11; backward 500 rows of
-  // 64 14.9 and 8.5 us, 14 k 19.8 and 18.0).  Wider rows are quicker streamed at every length (64 rows of 1024
-  // 4.0 and 3.9 us, 14 k 37 and 29).
+  // into a warp (14 k bf16 rows of 64 forward 4.3 us and streamed 8.6, of 130 already 21 and 11).  Backward, registers
+  // and streamed, token gate, bf16: rows of 64 14.7 and 8.1 us at 500 rows, 16.9 and 14.9 at 8 k, 19.6 and 21.1 at
+  // 16 k, 30.2 and 58.1 at 64 k; rows of 100 are quicker streamed at every length (32.8 and 25.7 at 16 k).  Wider
+  // rows are too (64 rows of 1024 4.0 and 3.9 us, 14 k 37 and 29).
   if (d < 128 && (!backward || T > 8192)) return p;
   const int most = backward ? kMaxBwd : kMaxFwd;
   int nv = most / 2;
@@ -738,7 +742,6 @@ StreamPlan stream_plan(int64_t T, int d, int dtype, bool backward, int gate_kind
   int64_t groups = (int64_t)device_sm_count() * (warps / w);
   if (groups > T) groups = T;
   const uint32_t row = (uint32_t)(nv * 32 * vec * es + (aligned ? 0 : 32)) * tensors * warps;   // of every warp
-  if (kStages * row > kRingBytes) return p;
   p.nv = nv;
   p.warps_row = w;
   p.warps = warps;
