@@ -420,7 +420,11 @@ GDPA_API gdpa_status_t gdpa_cache_append(const gdpa_rotary_t* r, const gdpa_cach
  *   to no sample do not count, so T may exceed B * max_n.  gdpa_chunk_workspace_size takes the samples' tokens
  *   alone, at most B * max_n (its result does not depend on them).
  *   Cache rows that no new token of the sample sees may hold anything (NaN too), and pages
- *   without such rows need no valid table entry.
+ *   without a row that one sees need no valid table entry.  Of a row that one sees, a key that is not finite
+ *   reaches only the tokens that see it; a value that is not finite may reach the sample's other tokens with heads of
+ *   that kv head (0 times infinity).
+ *   The probabilities are rounded to bf16 before their product with v, their sum is taken before that: with o's own
+ *   rounding o is off by up to 2^-8 (sum_p softmax_p |v_p| + |o|) (a root mean square of about 2.2e-3 of o).
  *   workspace: device, >= gdpa_chunk_workspace_size bytes, 256-byte aligned, of its own
  *   for every call that may run beside another one;
  *   its status word receives GDPA_ERR_INVALID_ARG for offsets that decrease,

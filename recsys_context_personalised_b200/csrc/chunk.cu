@@ -335,8 +335,8 @@ chunk_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 1));
             big[row] = fmaxf(big[row], __shfl_xor_sync(0xffffffffu, big[row], 2));
           }
-          // a row's offset moves only when its maximum grew by more than 2^8 (softmax does
-          // not depend on the offset, and 2^8 is far from overflow).  Each row decides for itself, and one that stays
+          // a row's offset moves only when its maximum grew by more than 2^8 (a published device of attention kernels:
+          // softmax does not depend on the offset, and 2^8 is far from overflow).  Each row decides for itself, and one that stays
           // is scaled by exactly 1: the tile's rows behind the item hold what was there before (or other
           // samples' queries) and must not change a bit of the others
           bool move[2];

@@ -15,7 +15,9 @@
 
 namespace gdpa {
 
-// sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0, m > 0 (Euclid-like descent)
+// sum of floor((a i + b) / m) over 0 <= i < n, for a, b >= 0, m > 0: the lattice points under a line, by the known
+// descent of Euclid's algorithm.  Whole multiples of m in a and b are sums in closed form; what is left lies under a line
+// of slope below 1, whose points are counted along the other axis, where a and m have changed places.
 GDPA_HD int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
   int64_t ans = 0;
   while (n > 0) {

@@ -24,8 +24,8 @@
 // bf16) aliases the first 64 columns of S_X, so S_X(j+1) is issued behind PV_X(j).  P goes out in two
 // halves of 64 keys; the product of the first runs while the second is computed.
 //
-// Softmax: online, the running offset kept while a block's maximum stays within 2^8 of it
-// (softmax does not depend on the offset, and 2^8 is far from overflow).  P is rounded to
+// Softmax: online, the running offset kept while a block's maximum stays within 2^8 of it (a published device of
+// attention kernels: softmax does not depend on the offset, and 2^8 is far from overflow).  P is rounded to
 // bf16, the precision of the MMA's operand; its sum l is taken before that.
 //
 // The code is kept short and its rare parts out of line: a launch fetches it cold, and the warps

@@ -1,5 +1,6 @@
 """The attention layer's operators at the edges of their calls, on the GPU: rows of a tile that no token
-owns, padded batches, waits that run out, whole numbers beyond 32 bits.  Helpers: test_gpu_layer."""
+owns, padded batches, waits that run out, whole numbers beyond 32 bits,
+values that are not finite.  Helpers: test_gpu_layer."""
 import ctypes
 
 import numpy as np
@@ -198,3 +199,54 @@ def test_windows_and_bounds_beyond_32_bits(n):
             G.chunk_fwd(*args, max_n=max_n)
     o, _ = G.chunk_fwd(*args, max_n=np.int64(max(n)), window=np.int32(7))
     assert torch.equal(o, G.chunk_fwd(*args, max_n=max(n), window=7)[0])
+
+
+# ------------------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("hq,hk,dh", [(2, 2, 64), (6, 2, 128), (40, 2, 32)])
+@pytest.mark.parametrize("n,at", [([4, 1], 2), ([200, 3], 130)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_values_that_are_not_finite(hq, hk, dh, n, at, value):
+    """In the key row of a new token they reach the tokens that see it and no other; in its value row they may
+    reach the sample's other tokens (0 times infinity), and no other sample or kv head."""
+    kv = [n[0] + 300, 150]
+    off, offd, table, ck, cv, q, scale = _chunk_case(n, kv, hq, hk, dh, 16, 49)
+    pos, group = kv[0] - n[0] + at, hq // hk
+    place = (int(table[0, pos // 16]), 0, pos % 16)
+
+    def call(k, v):
+        return G.chunk_fwd(q.to(DEV), offd, _int32(kv), _int32(table), k.to(DEV), v.to(DEV), scale, max_n=max(n))
+    want, wl = call(ck, cv)
+    bad = ck.clone()
+    bad[place] = value
+    o, lse = call(bad, cv)
+    mine = torch.zeros(off[-1], hq, dtype=torch.bool, device=DEV)
+    mine[at:n[0], :group] = True              # what sees the row
+    assert torch.equal(o[~mine], want[~mine]) and torch.equal(lse.T[~mine], wl.T[~mine])
+    if value != value:
+        assert not torch.isfinite(o[mine]).any()
+    bad = cv.clone()
+    bad[place] = value
+    o, lse = call(ck, bad)
+    assert not torch.isfinite(o[mine]).any()
+    mine[:n[0], :group] = True                # the sample's tokens with the heads of the kv head
+    assert torch.equal(o[~mine], want[~mine]) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d", [64, 1001, 4096])
+def test_a_norm_keeps_a_row_that_is_not_finite_to_itself(d, value):
+    """Other rows' results and their gate's gradient keep their bits."""
+    t, rnd = _norm_case(600, d, torch.float32, "token", True, True, 50)
+    dy, dn = rnd(600, d).to(DEV), rnd(600, d).to(DEV)
+
+    def both(f):
+        a = {k: v.to(DEV) for k, v in t.items()}
+        a["f"] = f.to(DEV)
+        y, n = G.block_norm_fwd(**a, sigmoid=True)
+        return y, n, *G.block_norm_bwd(y, a["f"], a["gate"], a["w_post"], a["w_pre"], dy, dn, sigmoid=True)[:3]
+    want = both(t["f"])
+    bad = t["f"].clone()
+    bad[300, d // 2] = value
+    keep = torch.arange(600, device=DEV) != 300
+    for a, b in zip(both(bad), want):
+        assert torch.equal(a[keep], b[keep]) and not torch.isfinite(a[300]).all()
