@@ -5,8 +5,8 @@
 // columns in flight by bulk copies into a ring of its own: the copies need no registers, so the
 // bytes in flight (about 100 KB an SM) do not depend on what the arithmetic holds, and a row's
 // reductions are shuffles within a warp, or a barrier of a row's few warps, that no other row waits for.
-// Measured (copy: 6.5 TB/s): 132 k rows of 2048 bf16 with a gate per element forward 447 us, 6.1 TB/s; 126 k rows
-// of 1024 backward, with a gate per element 364 us, 5.7 TB/s, with shared gates 280 us, 5.5 TB/s.
+// Measured (copy: 6.5 TB/s): 132 k rows of 2048 bf16 with a gate per element forward 483 us, 5.6 TB/s; backward 66 k
+// rows of 1024 with a gate per element 197 us, 5.4 TB/s, 126 k rows with shared gates 303 us, 5.1 TB/s.
 //
 // The weights' gradients (and a shared gate's) accumulate in fp32 registers over the range, in the
 // rows' order, and go to the workspace once.

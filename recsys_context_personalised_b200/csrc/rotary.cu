@@ -14,7 +14,7 @@
 // tokens with all their heads: it first writes the (cos, sin) of its tokens to
 // shared memory, once for all heads; then a thread takes the (cos, sin) of one piece of a token's heads into
 // registers and walks the heads with it in 16-byte vectors.  Measured (copy: 6.5 TB/s): 144 k tokens of 32
-// bf16 heads of 64 193 us, 6.1 TB/s; the append of 49 k tokens, 32 + 8 + 8 heads of 128, 206 us, 5.8 TB/s.
+// bf16 heads of 64 199 us, 5.9 TB/s; the append of 49 k tokens, 32 + 8 + 8 heads of 128, 206 us, 5.8 TB/s.
 #include <math.h>
 #include <stdio.h>
 

@@ -467,7 +467,7 @@ class _On:
         self.tensors = tensors if stream is not None else ()
         if stream is not None:
             at = getattr(stream, "device", None)
-            if at is not None and at.index not in (None, dev):
+            if getattr(at, "index", at) not in (None, dev):
                 raise GdpaError(1, f"stream of {at} for tensors on cuda:{dev}")
             if not isinstance(stream, torch.cuda.Stream):
                 raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
